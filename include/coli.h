@@ -286,6 +286,55 @@ COLI_API coli_status coli_moe_forward_host(const coli_moe_layer* layer, const vo
                                            coli_dtype xt, int T, void* out_host, void* out_dev, coli_dtype ot,
                                            void* workspace, size_t ws_bytes, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Routers of other decoders than the layer's own ("Colibri 完全ガイド", section
+ * コア技術のハイライト, names the DeepSeek-V3-style router; group-limited selection
+ * and softmax scores are this library's reading of that family).
+ */
+typedef enum { COLI_SCORE_SIGMOID = 0, COLI_SCORE_SOFTMAX = 1 } coli_score;
+
+typedef struct coli_router {
+    int hidden;            /* H: a multiple of 8, at most 16384 */
+    int n_experts;         /* E: 1 .. 1024 */
+    int top_k;             /* k: 1 .. 32, at most topk_group * (E / n_group) */
+    coli_score score;      /* of the E scores of a token */
+    int n_group;           /* groups of E / n_group consecutive experts (1 .. 32, divides E); 1: no groups */
+    int topk_group;        /* groups whose experts are eligible, 1 .. n_group */
+    int group_top;         /* a group's score is the sum of its 1 or 2 best choice scores */
+    int renormalise;       /* 1: the k weights sum to routed_scale; 0: routed_scale * score */
+    float routed_scale;
+    const float* w_router; /* [E, H] fp32 */
+    const float* sel_bias; /* [E] fp32, selection only, or NULL; -inf takes an expert out of the choice
+                              as long as k others are eligible */
+} coli_router;
+
+/* Bytes of workspace coli_router_forward needs for T tokens (0 if the router
+ * description or T is invalid).  Decided by the shapes alone. */
+COLI_API size_t coli_router_workspace_size(const coli_router* router, int T);
+
+/*
+ * Route with any coli_router.  For each token t of x [T, H] (dtype xt):
+ *   z_e = x_t . w_router[e];  s_e = 1/(1+exp(-z_e)) or exp(z_e) / sum exp(z);  c_e = s_e + sel_bias[e]
+ *   the topk_group groups of largest group score are eligible (equal: lower group first)
+ *   topk_idx[t, :] = the k eligible experts of largest c_e, descending (equal: lower expert first)
+ *   topk_w[t, j]   = routed_scale * s_idx[j], divided by sum_j' s_idx[j'] with renormalise
+ * Scores are summed in fp32 (weights to about 1e-6); the selection is that of
+ * double-precision sums: a decision closer than fp32 sums can carry is taken
+ * from double sums of the experts concerned, so a token routes alike whether it
+ * comes alone or in a batch (unless its scores cancel to far below the token's
+ * largest score).  A score that is NaN ranks last.  A token with a non-finite
+ * activation gets k distinct experts and unspecified weights; other tokens are
+ * not affected.
+ * Outputs: topk_idx int32 [T, k], topk_w fp32 [T, k] (device); x 16-byte
+ * aligned.  The workspace (256-byte aligned, contents undefined on entry) is not
+ * shared by calls that may run concurrently; after the call its first 4 bytes
+ * are a status word, 0 after a normal call (1: a pipeline wait of the batch
+ * kernel ran out, outputs undefined).  T == 0 launches nothing.
+ */
+COLI_API coli_status coli_router_forward(const coli_router* router, const void* x, coli_dtype xt, int T,
+                                         int32_t* topk_idx, float* topk_w, void* workspace, size_t ws_bytes,
+                                         cudaStream_t stream);
+
 COLI_API const char* coli_status_string(coli_status status);
 COLI_API const char* coli_last_error(void);
 

@@ -48,6 +48,10 @@ _lib.coli_status_string.restype = ctypes.c_char_p
 _lib.coli_status_string.argtypes = [_i]
 _lib.coli_last_error.restype = ctypes.c_char_p
 _lib.coli_last_error.argtypes = []
+_lib.coli_router_workspace_size.restype = ctypes.c_size_t
+_lib.coli_router_workspace_size.argtypes = [_p, _i]
+_lib.coli_router_forward.restype = _i
+_lib.coli_router_forward.argtypes = [_p, _p, _i, _i, _p, _p, _p, ctypes.c_size_t, _p]
 _lib.coli_debug_set_wait_ns.restype = None
 _lib.coli_debug_set_wait_ns.argtypes = [ctypes.c_ulonglong]
 _lib.coli_debug_phase_stamps.restype = None
@@ -67,6 +71,12 @@ class _LayerStruct(ctypes.Structure):
                 ("gate_q", _p), ("up_q", _p), ("down_q", _p),
                 ("gate_s", _p), ("up_s", _p), ("down_s", _p), ("top_p", ctypes.c_float),
                 ("act_int8", ctypes.c_int), ("prefetch_next", _p)]
+
+
+class _RouterStruct(ctypes.Structure):
+    _fields_ = [("hidden", _i), ("n_experts", _i), ("top_k", _i), ("score", _i), ("n_group", _i),
+                ("topk_group", _i), ("group_top", _i), ("renormalise", _i), ("routed_scale", ctypes.c_float),
+                ("w_router", _p), ("sel_bias", _p)]
 
 
 def lib():
@@ -136,6 +146,57 @@ def router_topk(x, w_router, sel_bias, k, routed_scale, topk_idx, topk_w, stream
     E = w_router.shape[0]
     _check(_lib.coli_router_topk(_ptr(x), _dtype_code(x), T, H, _ptr(w_router), _ptr(sel_bias), E, k,
                                  float(routed_scale), _ptr(topk_idx), _ptr(topk_w), _stream(stream)))
+
+
+SCORES = {"sigmoid": 0, "softmax": 1}
+
+
+def _check_tensor(t, name, shape, dtypes):
+    """Refuse a tensor the C calls would misread: they take bare pointers."""
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+
+
+class Router:
+    """A router: weights [E, H] fp32, an optional selection bias [E] fp32 and
+    how the experts are scored, grouped and weighted; see coli_router in
+    include/coli.h."""
+
+    def __init__(self, hidden, n_experts, top_k, w_router, sel_bias=None, score="sigmoid", n_group=1, topk_group=1,
+                 group_top=2, renormalise=True, routed_scale=1.0):
+        import torch
+        _check_tensor(w_router, "w_router", (n_experts, hidden), (torch.float32,))
+        if sel_bias is not None:
+            _check_tensor(sel_bias, "sel_bias", (n_experts,), (torch.float32,))
+        self.tensors = dict(w_router=w_router, sel_bias=sel_bias)
+        self.hidden, self.n_experts, self.top_k = hidden, n_experts, top_k
+        self.struct = _RouterStruct(hidden, n_experts, top_k, SCORES[score], n_group, topk_group, group_top,
+                                    1 if renormalise else 0, float(routed_scale), _ptr(w_router), _ptr(sel_bias))
+        self.ref = ctypes.byref(self.struct)
+
+
+def router_workspace_size(router, T):
+    """Bytes of workspace router_forward needs for T tokens."""
+    n = int(_lib.coli_router_workspace_size(router.ref, T))
+    if n == 0:
+        raise ColiError(1)
+    return n
+
+
+def router_forward(router, x, topk_idx, topk_w, workspace, stream=None):
+    """Route x [T, H]: topk_idx [T, k] int32 and topk_w [T, k] fp32 are written.
+    The first 4 bytes of the workspace are the call's status word."""
+    import torch
+    T = x.shape[0]
+    _check_tensor(x, "x", (T, router.hidden), (torch.bfloat16, torch.float32))
+    _check_tensor(topk_idx, "topk_idx", (T, router.top_k), (torch.int32,))
+    _check_tensor(topk_w, "topk_w", (T, router.top_k), (torch.float32,))
+    _check(_lib.coli_router_forward(router.ref, _ptr(x), _dtype_code(x), T, _ptr(topk_idx), _ptr(topk_w),
+                                    _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 def expert_union(topk_idx, E, count, offset, active, n_active, perm, inv_perm, stream=None):

@@ -1,6 +1,7 @@
 """Build libcoli.so (sm_100a) in-tree with nvcc."""
 import glob
 import os
+import re
 import subprocess
 import sys
 
@@ -9,6 +10,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libcoli.so")
+OBJ = os.path.join(PKG, "build")  # object files, not committed
 # the bounds-checked build: index checks record status 4 in the call's status word instead of trapping
 LIB_BOUNDS = os.path.join(PKG, "libcoli_bounds.so")
 
@@ -28,6 +30,20 @@ def _deps():
     return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
+def _includes(src):
+    """The source and every file of this tree that it includes, directly or not."""
+    seen, todo = set(), [src]
+    while todo:
+        path = todo.pop()
+        if path in seen:
+            continue
+        seen.add(path)
+        with open(path) as f:
+            names = re.findall(r'#include "([^"]+)"', f.read())
+        todo += [p for n in names for p in (os.path.join(CSRC, n), os.path.join(INCLUDE, n)) if os.path.exists(p)]
+    return seen
+
+
 def build(force=False, verbose=False, extra=(), bounds=False):
     """Build libcoli.so, or with bounds=True the bounds-checked libcoli_bounds.so."""
     out = LIB_BOUNDS if bounds else LIB
@@ -35,14 +51,26 @@ def build(force=False, verbose=False, extra=(), bounds=False):
         return out
     nvcc = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "bin", "nvcc")
     flags = [*NVCC_FLAGS, *extra] + (["-DCOLI_DEBUG_BOUNDS"] if bounds else [])
-    cmd = [nvcc, *flags, "-I", INCLUDE, "-I", CSRC, "-shared", "-o", out + ".tmp", *sources()]
-    if verbose:
-        print(" ".join(cmd))
-    subprocess.check_call(cmd)
+    # one object per source, compiled side by side; a source whose own includes are no newer keeps its object
+    objs, jobs = [], []
+    os.makedirs(OBJ, exist_ok=True)
+    for src in sources():
+        obj = os.path.join(OBJ, os.path.basename(src)[:-3] + ("_bounds.o" if bounds else ".o"))
+        objs.append(obj)
+        if not force and os.path.exists(obj) and os.path.getmtime(obj) >= max(os.path.getmtime(p) for p in _includes(src)):
+            continue
+        cmd = [nvcc, *flags, "-I", INCLUDE, "-I", CSRC, "-c", "-o", obj, src]
+        if verbose:
+            print(" ".join(cmd))
+        jobs.append((cmd, subprocess.Popen(cmd)))
+    failed = [cmd for cmd, p in jobs if p.wait() != 0]
+    if failed:
+        raise subprocess.CalledProcessError(1, failed[0])
+    subprocess.check_call([nvcc, *NVCC_FLAGS, "-shared", "-o", out + ".tmp", *objs])
     os.replace(out + ".tmp", out)
     return out
 
 
 if __name__ == "__main__":
     extra = ["-Xptxas", "-v"] if "-v" in sys.argv else []
-    print(build(force=True, verbose=True, extra=extra, bounds="--bounds" in sys.argv))
+    print(build(force="-f" in sys.argv or "-v" in sys.argv, verbose=True, extra=extra, bounds="--bounds" in sys.argv))

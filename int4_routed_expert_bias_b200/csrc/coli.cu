@@ -18,6 +18,7 @@
 #include "coli.h"
 #include "coli_common.cuh"
 #include "coli_decode.cuh"
+#include "coli_host.h"
 #include "coli_layer.cuh"
 #include "coli_prefill.cuh"
 #include "coli_router.cuh"
@@ -34,13 +35,12 @@ std::atomic<unsigned long long*> g_stamps{nullptr};
 
 // Test hook: limit of the kernels' bounded waits (0 = the built-in limits).
 std::atomic<unsigned long long> g_wait_ns{0};
-unsigned long long wait_limit(unsigned long long dflt)
-{
-    const unsigned long long v = g_wait_ns.load(std::memory_order_relaxed);
-    return v ? v : dflt;
-}
 thread_local cudaEvent_t* g_prof_events = nullptr;
 thread_local int g_prof_n = 0;
+
+}  // namespace
+
+namespace coli {
 
 coli_status fail(coli_status st, const char* fmt, ...)
 {
@@ -56,9 +56,15 @@ coli_status cuda_fail(cudaError_t e, const char* what)
     return fail(COLI_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+unsigned long long wait_limit(unsigned long long dflt)
+{
+    const unsigned long long v = g_wait_ns.load(std::memory_order_relaxed);
+    return v ? v : dflt;
+}
 
-constexpr int kMaxTokens = 65536;
+}  // namespace coli
+
+namespace {
 
 // Batches above this size take the tensor-core prefill path.
 constexpr int kDecodeMaxT = 64;
@@ -354,25 +360,6 @@ coli_status launch_logits(const void* x, coli_dtype xt, int T, int H, const floa
         router_logits_kernel<false><<<grid, kRouterThreads, 0, s>>>(x, T, H, w_router, E, logits, zero_ctr, n_zero);
     cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? COLI_OK : cuda_fail(e, "router launch");
-}
-
-// Launch as a programmatic dependent of the previous kernel on the stream: its
-// launch may overlap the predecessor's tail; the kernel calls griddep_wait()
-// before it reads anything the predecessor wrote.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kern)(KArgs...), int grid, int block, size_t smem, cudaStream_t s, Args... args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(block);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 // cuTensorMapEncodeTiled from the CUDA driver, looked up once (the library links

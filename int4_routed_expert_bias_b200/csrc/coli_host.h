@@ -1,0 +1,54 @@
+// coli_host.h -- host-side helpers shared by the library's translation units:
+// error reporting, argument checks and launch helpers.  Internal to libcoli.so.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "coli.h"
+
+namespace coli {
+
+constexpr int kMaxTokens = 65536;
+
+// Record a message for coli_last_error() of this thread and return st.
+coli_status fail(coli_status st, const char* fmt, ...);
+coli_status cuda_fail(cudaError_t e, const char* what);
+
+// The limit of the kernels' bounded waits: the test hook's value if set, else dflt.
+unsigned long long wait_limit(unsigned long long dflt);
+
+inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+// Whether byte ranges [a, a + na) and [b, b + nb) share a byte.
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb)
+{
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return a && b && x < y + nb && y < x + na;
+}
+
+inline bool known_dtype(coli_dtype t) { return t == COLI_F32 || t == COLI_BF16; }
+inline size_t dtype_size(coli_dtype t) { return t == COLI_BF16 ? 2 : 4; }
+
+// Launch as a programmatic dependent of the previous kernel on the stream: its
+// launch may overlap the predecessor's tail; the kernel calls griddep_wait()
+// before it reads anything the predecessor wrote.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, int block, size_t smem, cudaStream_t s, Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+}  // namespace coli

@@ -1,0 +1,142 @@
+// coli_route.cu -- host side of the general router (coli_router_forward).
+#include <algorithm>
+#include <cmath>
+
+#include "coli_host.h"
+#include "coli_route.cuh"
+
+using namespace coli;
+
+namespace {
+
+constexpr size_t kStatusBytes = 256;  // the status word and its padding, at the start of the workspace
+
+coli_status check_router(const coli_router* r, int T)
+{
+    if (!r) return fail(COLI_ERR_INVALID_ARG, "router is NULL");
+    if (T < 0 || T > kMaxTokens) return fail(COLI_ERR_INVALID_ARG, "T=%d outside [0, %d]", T, kMaxTokens);
+    if (r->hidden <= 0 || r->hidden % 8 != 0 || r->hidden > 16384)
+        return fail(COLI_ERR_INVALID_ARG, "hidden=%d is not a multiple of 8 in [8, 16384]", r->hidden);
+    if (r->n_experts < 1 || r->n_experts > kMaxExperts)
+        return fail(COLI_ERR_INVALID_ARG, "n_experts=%d outside [1, %d]", r->n_experts, kMaxExperts);
+    if (r->score != COLI_SCORE_SIGMOID && r->score != COLI_SCORE_SOFTMAX)
+        return fail(COLI_ERR_INVALID_ARG, "unknown score function %d", (int)r->score);
+    if (r->n_group < 1 || r->n_group > kRouteMaxGroups || r->n_experts % r->n_group != 0)
+        return fail(COLI_ERR_INVALID_ARG, "n_group=%d is not a divisor of n_experts=%d in [1, %d]", r->n_group, r->n_experts,
+                    kRouteMaxGroups);
+    if (r->topk_group < 1 || r->topk_group > r->n_group)
+        return fail(COLI_ERR_INVALID_ARG, "topk_group=%d outside [1, n_group=%d]", r->topk_group, r->n_group);
+    const int m = r->n_experts / r->n_group;
+    if ((r->group_top != 1 && r->group_top != 2) || (r->n_group > 1 && r->group_top > m))
+        return fail(COLI_ERR_INVALID_ARG, "group_top=%d (1 or 2, at most the group's %d experts)", r->group_top, m);
+    if (r->top_k < 1 || r->top_k > kMaxTopK || r->top_k > r->topk_group * m)
+        return fail(COLI_ERR_INVALID_ARG, "top_k=%d outside [1, %d] (at most %d, and the %d eligible experts)", r->top_k,
+                    std::min(kMaxTopK, r->topk_group * m), kMaxTopK, r->topk_group * m);
+    if (r->renormalise != 0 && r->renormalise != 1) return fail(COLI_ERR_INVALID_ARG, "renormalise=%d (0 or 1)", r->renormalise);
+    if (!std::isfinite(r->routed_scale)) return fail(COLI_ERR_INVALID_ARG, "routed_scale is not finite");
+    if (!r->w_router) return fail(COLI_ERR_INVALID_ARG, "router.w_router is NULL");
+    if (!aligned(r->w_router, 16)) return fail(COLI_ERR_INVALID_ARG, "router.w_router is not 16-byte aligned");
+    if (!aligned(r->sel_bias, 4)) return fail(COLI_ERR_INVALID_ARG, "router.sel_bias is not 4-byte aligned");
+    return COLI_OK;
+}
+
+// How a call is cut, from the shapes alone.
+struct RoutePlan {
+    int mt;      // row kernel: tokens per warp pass
+    int splits;  // pieces of K, summed by the selection kernel in order
+    int chunk;   // K values of a piece
+    int Ep;
+    size_t bytes;  // workspace
+};
+
+RoutePlan route_plan(int T, int H, int E)
+{
+    RoutePlan p{};
+    p.Ep = (E + 3) & ~3;
+    p.mt = T >= 8 ? 8 : T >= 4 ? 4 : T >= 2 ? 2 : 1;
+    // enough pieces that a call of few tokens has about 14 warps on every SM,
+    // each at least 128 lanes' worth of 16-byte loads long
+    const long long units = (long long)E * std::max(1, (T + p.mt - 1) / p.mt);
+    const int most = std::max(1, std::min(8, (H + 127) / 128));
+    p.splits = (int)std::max(1ll, std::min((long long)most, (14ll * kRouteSms + units - 1) / units));
+    p.chunk = ((H + p.splits - 1) / p.splits + 127) / 128 * 128;
+    p.splits = (H + p.chunk - 1) / p.chunk;
+    p.bytes = kStatusBytes + align_up((size_t)p.splits * T * p.Ep * 4, 256);
+    return p;
+}
+
+template <bool kBf16>
+cudaError_t launch_rows(const RouteArgs& a, int mt, cudaStream_t s)
+{
+    const dim3 grid((a.E * a.splits + kRouteWarps - 1) / kRouteWarps, (a.T + mt - 1) / mt);
+    switch (mt) {
+        case 1: route_rows_kernel<1, kBf16><<<grid, kRouteThreads, 0, s>>>(a); break;
+        case 2: route_rows_kernel<2, kBf16><<<grid, kRouteThreads, 0, s>>>(a); break;
+        case 4: route_rows_kernel<4, kBf16><<<grid, kRouteThreads, 0, s>>>(a); break;
+        default: route_rows_kernel<8, kBf16><<<grid, kRouteThreads, 0, s>>>(a); break;
+    }
+    return cudaGetLastError();
+}
+
+template <bool kBf16>
+cudaError_t launch_select(const RouteArgs& a, cudaStream_t s)
+{
+    const size_t per = route_token_smem(a.E);
+    const int most = std::max(1, std::min(kRouteWarps, (int)(49152 / per)));
+    const int tokens = std::max(1, std::min(most, (a.T + 2 * kRouteSms - 1) / (2 * kRouteSms)));
+    const dim3 grid((a.T + tokens - 1) / tokens);
+    auto go = [&](auto kern) { return launch_pdl(kern, grid, kRouteThreads, tokens * per, s, a, tokens); };
+    const int n = (a.E + 31) / 32;
+    if (n <= 1) return go(route_select_kernel<1, kBf16>);
+    if (n <= 2) return go(route_select_kernel<2, kBf16>);
+    if (n <= 4) return go(route_select_kernel<4, kBf16>);
+    if (n <= 8) return go(route_select_kernel<8, kBf16>);
+    if (n <= 16) return go(route_select_kernel<16, kBf16>);
+    return go(route_select_kernel<32, kBf16>);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t coli_router_workspace_size(const coli_router* r, int T)
+{
+    if (check_router(r, T) != COLI_OK) return 0;
+    return route_plan(T, r->hidden, r->n_experts).bytes;
+}
+
+coli_status coli_router_forward(const coli_router* r, const void* x, coli_dtype xt, int T, int32_t* topk_idx,
+                                float* topk_w, void* workspace, size_t ws_bytes, cudaStream_t stream)
+{
+    coli_status st = check_router(r, T);
+    if (st != COLI_OK) return st;
+    if (!known_dtype(xt)) return fail(COLI_ERR_INVALID_ARG, "unknown activation dtype %d", (int)xt);
+    if (T == 0) return COLI_OK;
+    if (!x || !topk_idx || !topk_w || !workspace) return fail(COLI_ERR_INVALID_ARG, "NULL pointer argument");
+    if (!aligned(x, 16)) return fail(COLI_ERR_INVALID_ARG, "x not 16-byte aligned");
+    if (!aligned(topk_idx, 4) || !aligned(topk_w, 4)) return fail(COLI_ERR_INVALID_ARG, "routing outputs not 4-byte aligned");
+    if (!aligned(workspace, 256)) return fail(COLI_ERR_INVALID_ARG, "workspace not 256-byte aligned");
+    const RoutePlan p = route_plan(T, r->hidden, r->n_experts);
+    if (ws_bytes < p.bytes) return fail(COLI_ERR_WORKSPACE, "workspace %zu bytes, need %zu", ws_bytes, p.bytes);
+
+    RouteArgs a{};
+    a.T = T, a.H = r->hidden, a.E = r->n_experts, a.k = r->top_k;
+    a.softmax = r->score == COLI_SCORE_SOFTMAX;
+    a.groups = r->topk_group == r->n_group ? 1 : r->n_group;  // every group kept: no groups
+    a.keep = a.groups == 1 ? 1 : r->topk_group;
+    a.top = r->group_top;
+    a.renorm = r->renormalise;
+    a.scale = r->routed_scale;
+    a.x = x, a.w_router = r->w_router, a.bias = r->sel_bias;
+    a.status = static_cast<int*>(workspace);
+    a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kStatusBytes);
+    a.splits = p.splits, a.Ep = p.Ep, a.chunk = p.chunk;
+    a.idx = topk_idx, a.w = topk_w;
+    const bool bf16 = xt == COLI_BF16;
+    cudaError_t e = bf16 ? launch_rows<true>(a, p.mt, stream) : launch_rows<false>(a, p.mt, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "router score launch");
+    e = bf16 ? launch_select<true>(a, stream) : launch_select<false>(a, stream);
+    return e == cudaSuccess ? COLI_OK : cuda_fail(e, "router selection launch");
+}
+
+}  // extern "C"

@@ -1,0 +1,568 @@
+// coli_route.cuh -- the general router (coli_router_forward): scores of fp32
+// router weights, sigmoid or softmax, selection bias, groups of experts, the k
+// best experts in order and their weights.
+//
+//   z_e = x . w_e;  s = sigmoid(z) or softmax(z);  c_e = s_e + bias_e
+//   score of a group = sum of its `top` best c (1 or 2); the `keep` best groups are eligible
+//   idx = the k eligible experts of largest c, descending (equal c: lower index)
+//   w_j = scale * s_j, divided by the sum of the selected s when renormalised
+//
+// Which of two experts comes first is decided by the last bits of their scores,
+// so fp32 sums of different kernels (one token, a batch) would disagree now and
+// then.  Here the selection is that of 64-bit arithmetic: the scores are summed
+// in fp32, every decision that takes part in the answer (adjacent selected
+// experts, the last selected against the first rejected one, the last eligible
+// group against the first rejected one) is checked against the largest error
+// those sums can carry, and where one is closer than that the experts concerned
+// are summed again in double, until all decisions are clear (route_exact).
+// That is rare and touches a few rows of x and W that are in L2.
+#pragma once
+
+#include "coli_common.cuh"
+
+namespace coli {
+
+constexpr int kRouteThreads = 256;
+constexpr int kRouteWarps = kRouteThreads / 32;
+constexpr int kRouteMaxGroups = 32;
+constexpr int kRouteSms = 148;      // grid sizing (B200); the results do not depend on it
+constexpr int kRouteRowsMT = 8;     // tokens per pass of the row kernel
+constexpr int kRouteMaxSplits = 64;
+
+// Error of an fp32 score sum that the selection allows for, relative to the token's largest |z|.
+constexpr float kRouteSumErr = 1.0f / 131072.0f;  // 2^-17
+
+struct RouteArgs {
+    int T, H, E, k;
+    int softmax;             // 0: sigmoid
+    int groups, keep, top;   // groups == 1: every expert is eligible
+    int renorm;
+    float scale;
+    const void* x;           // [T, H]
+    const float* w_router;   // [E, H]
+    const float* bias;       // [E] or null
+    int* status;             // the call's status word
+    float* part;             // [splits, T, Ep] partial scores
+    int splits, Ep;          // Ep: E rounded up to a multiple of 4
+    int chunk;               // K values of one split
+    int32_t* idx;            // [T, k]
+    float* w;                // [T, k]
+};
+
+// ---------------------------------------------------------------------------
+// Scores, row form: one warp per (expert, split of K, MT tokens).  Bound by the
+// read of W for one token (6.3 MB at hidden 6144, 256 experts); the splits put
+// every load of the call in flight at once.  fp32 multiply-adds in a fixed order.
+template <int MT, bool kBf16>
+__global__ void __launch_bounds__(kRouteThreads) route_rows_kernel(const __grid_constant__ RouteArgs a)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int unit = blockIdx.x * kRouteWarps + warp;
+    griddep_launch_dependents();
+    if (unit >= a.E * a.splits) return;
+    const int e = unit / a.splits, sp = unit - e * a.splits;
+    const int t0 = blockIdx.y * MT, nt = min(MT, a.T - t0);
+    const int k0 = sp * a.chunk, k1 = min(a.H, k0 + a.chunk);
+    const float* wrow = a.w_router + (size_t)e * a.H;
+    const size_t xrow = (size_t)a.H * (kBf16 ? 2 : 4);
+    const char* xb = static_cast<const char*>(a.x) + (size_t)t0 * xrow;
+    float acc[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) acc[t] = 0.f;
+    constexpr int kU = MT <= 2 ? 6 : 3;
+    for (int base = k0 + lane * 4; base < k1; base += kU * 128) {
+        float4 wv[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int i = base + u * 128;
+            wv[u] = i < k1 ? *reinterpret_cast<const float4*>(wrow + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            if (t < nt) {
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    const int i = base + u * 128;
+                    if (i < k1) {
+                        const float4 v = load_act4<kBf16>(xb + t * xrow, i);
+                        acc[t] = fmaf(wv[u].x, v.x, acc[t]);
+                        acc[t] = fmaf(wv[u].y, v.y, acc[t]);
+                        acc[t] = fmaf(wv[u].z, v.z, acc[t]);
+                        acc[t] = fmaf(wv[u].w, v.w, acc[t]);
+                    }
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+        const float v = warp_sum(acc[t]);
+        if (lane == 0 && t < nt) a.part[((size_t)sp * a.T + t0 + t) * a.Ep + e] = v;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Selection
+
+__device__ __forceinline__ float warp_max(float v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    return v;
+}
+__device__ __forceinline__ float warp_min(float v) { return -warp_max(-v); }
+
+// Order-preserving image of a float that is not NaN, above 0 (0 marks what cannot be chosen), and back.
+__device__ __forceinline__ uint32_t order_key(float c)
+{
+    const uint32_t u = __float_as_uint(c + 0.0f);  // -0 -> +0
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float order_value(uint32_t m)
+{
+    return __uint_as_float((m & 0x80000000u) ? (m & 0x7FFFFFFFu) : ~m);
+}
+
+// Bound on the error of an fp32 choice score c = s + bias, from the bound dz on
+// z: sigmoid' <= 1/4; softmax moves by at most 2 s dz (its own z and the sum);
+// a few units in the last place of s and of the sum with the bias.
+__device__ __forceinline__ float choice_err(int softmax, float s, float c, float dz)
+{
+    if (!(fabsf(c) < 3.0e38f)) return 0.f;  // an infinite bias decides by itself
+    const float own = softmax ? s * (2.f * dz + 0x1p-20f) : 0.25f * dz + 0x1p-22f;
+    return own + 0x1p-23f * fabsf(c);
+}
+
+// z = x_t . w_e in double by one warp (the same order for every expert, so equal rows stay equal).
+__device__ __forceinline__ double route_dot(const RouteArgs& a, bool bf16, int t, int e)
+{
+    const int lane = threadIdx.x & 31;
+    const float* wrow = a.w_router + (size_t)e * a.H;
+    const char* xr = static_cast<const char*>(a.x) + (size_t)t * a.H * (bf16 ? 2 : 4);
+    double s0 = 0., s1 = 0., s2 = 0., s3 = 0.;
+#pragma unroll 4
+    for (int i = lane * 4; i < a.H; i += 128) {
+        const float4 w = *reinterpret_cast<const float4*>(wrow + i);
+        const float4 v = bf16 ? load_act4<true>(xr, i) : load_act4<false>(xr, i);
+        s0 = fma((double)w.x, (double)v.x, s0);
+        s1 = fma((double)w.y, (double)v.y, s1);
+        s2 = fma((double)w.z, (double)v.z, s2);
+        s3 = fma((double)w.w, (double)v.w, s3);
+    }
+    double s = (s0 + s1) + (s2 + s3);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    return s;
+}
+
+__device__ __forceinline__ double warp_sum_d(double v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+__device__ __forceinline__ double warp_max_d(double v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmax(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    return v;
+}
+
+__device__ __forceinline__ double choice_d(const RouteArgs& a, const double* pd, int e)
+{
+    const double c = a.bias ? pd[e] + (double)a.bias[e] : pd[e];
+    return c == c ? c : -INFINITY;
+}
+// Error of a choice score still summed in fp32 (0 once it is summed in double, or decided by its bias).
+__device__ __forceinline__ double choice_err_d(const RouteArgs& a, double p, double c, bool exact, double dz)
+{
+    if (exact || !(fabs(c) < 1.0e300)) return 0.;
+    return a.softmax ? 2. * p * dz : 0.25 * dz;
+}
+
+// The selection of one token whose fp32 scores leave a decision open, by one
+// warp.  zd starts as the fp32 scores; `st[e]` is 1 once z_e is a double sum.
+// Each round selects with what is known, marks the experts of every open
+// decision that are not yet exact, and sums those in double; it ends when no
+// decision is open.  dz = 0: the scores are exact as they are.  For softmax with
+// a bias the denominator's own error also matters (c mixes s with a bias): it is
+// bounded by dz times the probability mass not yet exact, and the largest of
+// those are summed next.  Lane j < k returns slot j.
+__device__ __noinline__ void route_exact(const RouteArgs& a, bool bf16, int t, const float* z, double* zd, double* pd,
+                                         unsigned char* st, double dz, int& my_e, double& my_p)
+{
+    const int lane = threadIdx.x & 31;
+    const int E = a.E, G = a.groups, m = E / G;
+    const unsigned full = 0xFFFFFFFFu;
+    for (int e = lane; e < E; e += 32) {
+        zd[e] = (double)z[e];
+        st[e] = dz == 0. ? 1 : 0;
+    }
+    __syncwarp();
+    for (int round = 0; round <= E; ++round) {
+        double mass = 0.;  // softmax: probability of the experts not yet exact
+        if (a.softmax) {
+            double mx = -INFINITY, sum = 0.;
+            for (int e = lane; e < E; e += 32) mx = fmax(mx, zd[e]);
+            mx = warp_max_d(mx);
+            for (int e = lane; e < E; e += 32) sum += pd[e] = exp(zd[e] - mx);
+            sum = warp_sum_d(sum);
+            for (int e = lane; e < E; e += 32) {
+                pd[e] /= sum;
+                if (!st[e]) mass += pd[e];
+            }
+            mass = warp_sum_d(mass);
+        } else {
+            for (int e = lane; e < E; e += 32) pd[e] = 1. / (1. + exp(-zd[e]));
+        }
+        __syncwarp();
+        const double dd = a.softmax && a.bias ? dz * mass : 0.;  // relative error of the denominator
+        bool marked = false, need_mass = false;
+
+        // eligible groups: lane g < G holds group g
+        uint32_t kept = full;
+        if (G > 1) {
+            double b1 = -INFINITY, b2 = -INFINITY, gp = 0., gu = 0., last = 0., last_u = 0.;
+            int e1 = -1, e2 = -1;
+            if (lane < G) {
+                for (int e = lane * m; e < (lane + 1) * m; ++e) {
+                    const double c = choice_d(a, pd, e);
+                    if (e1 < 0 || c > b1) {
+                        b2 = b1, e2 = e1;
+                        b1 = c, e1 = e;
+                    } else if (e2 < 0 || c > b2) {
+                        b2 = c, e2 = e;
+                    }
+                }
+                gp = pd[e1];
+                gu = last_u = choice_err_d(a, pd[e1], b1, st[e1], dz);
+                last = b1;
+                if (a.top == 2) {
+                    last_u = choice_err_d(a, pd[e2], b2, st[e2], dz);
+                    gp += pd[e2];
+                    gu += last_u;
+                    last = b2;
+                }
+                // an expert outside the counted ones may belong among them
+                double extra = 0.;
+                for (int e = lane * m; e < (lane + 1) * m; ++e) {
+                    if (st[e]) continue;
+                    const double c = choice_d(a, pd, e), u = choice_err_d(a, pd[e], c, false, dz);
+                    if (c + u >= last - last_u) extra = fmax(extra, u);
+                }
+                gu += extra * a.top;
+            }
+            const double score = a.top == 2 ? b1 + b2 : b1;
+            int rank = 0;
+            for (int g = 0; g < G; ++g) {
+                const double o = __shfl_sync(full, score, g);
+                rank += (o > score || (o == score && g < lane)) ? 1 : 0;
+            }
+            const bool in = lane < G && rank < a.keep;
+            kept = __ballot_sync(full, in);
+            bool open = false;
+            for (int g = 0; g < G; ++g) {
+                const double o = __shfl_sync(full, score, g), ou = __shfl_sync(full, gu, g), op = __shfl_sync(full, gp, g);
+                if (lane < G && in != (((kept >> g) & 1u) != 0)) {
+                    const double bound = gu + ou + dd * fabs(gp - op);
+                    if (bound > 0. && fabs(score - o) <= bound) open = true;
+                }
+            }
+            if (open) {
+                for (int e = lane * m; e < (lane + 1) * m; ++e) {
+                    if (st[e]) continue;
+                    const double c = choice_d(a, pd, e), u = choice_err_d(a, pd[e], c, false, dz);
+                    if (c + u >= last - last_u) {
+                        st[e] = 2;
+                        marked = true;
+                    }
+                }
+                need_mass = dd > 0.;
+            }
+            __syncwarp();
+        }
+        auto eligible = [&](int e) { return G == 1 || ((kept >> (e / m)) & 1u); };
+
+        // the k best, in order
+        double my_c = 0.;
+        my_e = 0;
+        double prev_c = INFINITY;
+        int prev_e = -1;
+        for (int j = 0; j < a.k; ++j) {
+            double bc = -INFINITY;
+            int be = -1;
+            for (int e = lane; e < E; e += 32) {
+                if (!eligible(e)) continue;
+                const double c = choice_d(a, pd, e);
+                if (prev_e >= 0 && !(c < prev_c || (c == prev_c && e > prev_e))) continue;  // taken
+                if (be < 0 || c > bc) bc = c, be = e;
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                const double oc = __shfl_xor_sync(full, bc, o);
+                const int oe = __shfl_xor_sync(full, be, o);
+                if (oe >= 0 && (be < 0 || oc > bc || (oc == bc && oe < be))) bc = oc, be = oe;
+            }
+            prev_c = bc;
+            prev_e = be;
+            if (lane == j) my_c = bc, my_e = be;
+        }
+        my_p = pd[my_e];
+
+        // open decisions among the selected and against the rest
+        for (int j = 0; j < a.k; ++j) {
+            const double cj = __shfl_sync(full, my_c, j), pj = __shfl_sync(full, my_p, j);
+            const int ej = __shfl_sync(full, my_e, j);
+            const bool xj = st[ej] == 1;
+            const double uj = choice_err_d(a, pj, cj, xj, dz);
+            bool open_j = false;
+            for (int e = lane; e < E; e += 32) {
+                if (e == ej || !eligible(e)) continue;
+                const double c = choice_d(a, pd, e);
+                const bool xe = st[e] == 1;
+                const double bound = choice_err_d(a, pd[e], c, xe, dz) + uj + dd * fabs(pd[e] - pj);
+                if (!(bound > 0.) || !(fabs(c - cj) <= bound)) continue;
+                if (!xe) {
+                    st[e] = 2;
+                    marked = true;
+                }
+                if (!xj) open_j = true;
+                if (dd > 0.) need_mass = true;
+            }
+            open_j = __any_sync(full, open_j);
+            if (open_j && lane == 0) {
+                st[ej] = 2;
+                marked = true;
+            }
+            __syncwarp();
+        }
+        marked = __any_sync(full, marked);
+        need_mass = __any_sync(full, need_mass);
+        if (!marked && need_mass) {  // only the denominator is open: the largest terms not yet exact
+            double big = 0.;
+            for (int e = lane; e < E; e += 32)
+                if (!st[e]) big = fmax(big, pd[e]);
+            big = warp_max_d(big);
+            for (int e = lane; e < E; e += 32)
+                if (!st[e] && pd[e] >= 0.5 * big) {
+                    st[e] = 2;
+                    marked = true;
+                }
+            marked = __any_sync(full, marked);
+        }
+        if (!marked) break;
+        __syncwarp();
+        for (int b = 0; b < E; b += 32) {
+            uint32_t todo = __ballot_sync(full, b + lane < E && st[b + lane] == 2);
+            while (todo) {
+                const int e = b + __ffs(todo) - 1;
+                todo &= todo - 1;
+                const double v = route_dot(a, bf16, t, e);
+                if (lane == 0) {
+                    zd[e] = v;
+                    st[e] = 1;
+                }
+            }
+        }
+        __syncwarp();
+    }
+}
+
+// Shared memory of one token of the selection kernel: z [E] floats, then zd [E]
+// and pd [E] doubles (pd's place holds the fp32 choice scores, padded by one
+// per group, on the usual path), then a state byte per expert.
+__host__ __device__ __forceinline__ size_t route_token_smem(int E)
+{
+    const size_t pd = (size_t)E * 8 > (size_t)E * 4 + 128 ? (size_t)E * 8 : (size_t)E * 4 + 128;
+    return align_up((size_t)E * 4, 16) + align_up((size_t)E * 8, 16) + align_up(pd, 16) + align_up((size_t)E, 16);
+}
+
+// Selection: a block sums the partial scores of `tokens` tokens, one warp per
+// token selects.  kPer = experts per lane.  Latency-bound: k + 1 rounds of a
+// warp-wide maximum (one redux instruction) over order-preserving integer keys.
+template <int kPer, bool kBf16>
+__global__ void __launch_bounds__(kRouteThreads) route_select_kernel(const __grid_constant__ RouteArgs a, int tokens)
+{
+    extern __shared__ __align__(16) unsigned char route_smem[];
+    const unsigned full = 0xFFFFFFFFu;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int E = a.E, t0 = blockIdx.x * tokens, nt = min(tokens, a.T - t0);
+    const size_t stride = route_token_smem(E);
+    griddep_wait();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
+    {
+        const int Ep = a.Ep, Eq = Ep / 4;
+        const size_t plane = (size_t)a.T * Ep;
+        for (int i = threadIdx.x; i < nt * Eq; i += kRouteThreads) {
+            const int t = i / Eq, q = i - t * Eq;
+            const float* p = a.part + (size_t)(t0 + t) * Ep + 4 * q;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int s0 = 0; s0 < a.splits; s0 += 8) {  // eight independent loads at a time
+                float4 o[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    o[j] = s0 + j < a.splits ? *reinterpret_cast<const float4*>(p + (s0 + j) * plane)
+                                             : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v.x += o[j].x, v.y += o[j].y, v.z += o[j].z, v.w += o[j].w;
+            }
+            float* dst = reinterpret_cast<float*>(route_smem + t * stride) + 4 * q;
+            const float r[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (4 * q + j < E) dst[j] = r[j];
+        }
+    }
+    __syncthreads();
+    if (warp >= nt) return;
+    const int t = t0 + warp;
+    unsigned char* base = route_smem + warp * stride;
+    const float* z_s = reinterpret_cast<const float*>(base);
+    double* zd = reinterpret_cast<double*>(base + align_up((size_t)E * 4, 16));
+    double* pd = zd + align_up((size_t)E * 8, 16) / 8;
+    unsigned char* st = base + stride - align_up((size_t)E, 16);
+
+    float z[kPer], c[kPer];
+    float zmax = 0.f, zm = -INFINITY;
+    bool odd = false;  // a score that is not finite
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int e = lane + 32 * i;
+        z[i] = e < E ? z_s[e] : 0.f;
+        zmax = fmaxf(zmax, fabsf(z[i]));
+        odd |= !(fabsf(z[i]) < INFINITY);
+        if (e < E) zm = fmaxf(zm, z[i]);
+    }
+    zmax = warp_max(zmax);
+    zm = warp_max(zm);
+    const float dz = kRouteSumErr * zmax;
+    // s_e: the unbiased score
+    float den = 1.f;
+    if (a.softmax) {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (lane + 32 * i < E) sum += expf(z[i] - zm);
+        den = warp_sum(sum);
+    }
+    auto score_of = [&](float v) { return a.softmax ? expf(v - zm) / den : 1.0f / (1.0f + expf(-v)); };
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int e = lane + 32 * i;
+        c[i] = -INFINITY;
+        if (e < E) {
+            const float s = score_of(z[i]);
+            const float v = a.bias ? s + a.bias[e] : s;
+            c[i] = v == v ? v : -INFINITY;  // NaN ranks last: the order stays total
+        }
+    }
+
+    // eligible groups
+    uint32_t kept = full;
+    bool open = false;
+    const int G = a.groups, m = E / G;
+    if (G > 1) {
+        float* c_s = reinterpret_cast<float*>(pd);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int e = lane + 32 * i;
+            if (e < E) c_s[e + e / m] = c[i];
+        }
+        __syncwarp();
+        // 32 / 2^ceil(log2 G) lanes per group, each a strided share of its experts
+        int lg = 32;
+        while (lg > 1 && G * lg > 32) lg >>= 1;
+        const int g = lane / lg, r = lane - g * lg;
+        float b1 = -INFINITY, b2 = -INFINITY, u = 0.f;
+        if (g < G) {
+            for (int j = r; j < m; j += lg) {
+                const float v = c_s[g * (m + 1) + j];
+                if (v > b1) b2 = b1, b1 = v;
+                else if (v > b2) b2 = v;
+            }
+        }
+        for (int o = lg >> 1; o > 0; o >>= 1) {
+            const float o1 = __shfl_xor_sync(full, b1, o), o2 = __shfl_xor_sync(full, b2, o);
+            b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
+            b1 = fmaxf(b1, o1);
+        }
+        const float s_most = 1.f / den;  // no softmax score is larger
+        u = choice_err(a.softmax, s_most, b1, dz);
+        float score = b1;
+        if (a.top == 2) {
+            u += choice_err(a.softmax, s_most, b2, dz);
+            score = b1 + b2;
+        }
+        if (!(score == score)) score = -INFINITY;
+        int rank = 0;
+        for (int h = 0; h < G; ++h) {
+            const float o = __shfl_sync(full, score, h * lg);
+            rank += (o > score || (o == score && h < g)) ? 1 : 0;
+        }
+        const bool in = g < G && rank < a.keep;
+        kept = 0;
+        for (int h = 0; h < G; ++h) kept |= (__shfl_sync(full, (uint32_t)in, h * lg) & 1u) << h;
+        if (a.keep < G) {
+            const float lo = warp_min(in ? score : INFINITY), hi = warp_max(g < G && !in ? score : -INFINITY);
+            const float um = warp_max(g < G ? u : 0.f);
+            open = lo - hi <= 2.f * um;
+        }
+    }
+
+    uint32_t key[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int e = lane + 32 * i;
+        key[i] = e < E && (G == 1 || ((kept >> (e / m)) & 1u)) ? order_key(c[i]) : 0u;
+    }
+    // k rounds (and one more, for the gap to the first rejected expert)
+    int my_e = 0;
+    float my_c = 0.f, next_c = -INFINITY;
+    int next_e = -1;
+    const int rounds = a.k + (a.k < a.keep * m ? 1 : 0);
+    for (int j = 0; j < rounds; ++j) {
+        uint32_t best = key[0];
+        int bi = 0;
+#pragma unroll
+        for (int i = 1; i < kPer; ++i)
+            if (key[i] > best) best = key[i], bi = i;
+        const uint32_t top = __reduce_max_sync(full, best);
+        const int e = (int)__reduce_min_sync(full, best == top ? (uint32_t)(lane + 32 * bi) : 0xFFFFFFFFu);
+        if (lane == (e & 31)) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (i == (e >> 5)) key[i] = 0u;
+        }
+        const float v = order_value(top);
+        if (j == a.k) next_c = v, next_e = e;
+        else if (lane == j) my_e = e, my_c = v;
+    }
+    float my_s = score_of(z_s[my_e]);
+    {
+        // gaps between neighbours in rank against what the fp32 sums can carry
+        const float my_u = choice_err(a.softmax, my_s, my_c, dz);
+        float nc = __shfl_down_sync(full, my_c, 1), nu = __shfl_down_sync(full, my_u, 1);
+        bool has = lane + 1 < a.k;
+        if (lane == a.k - 1 && next_e >= 0) {
+            nc = next_c;
+            nu = choice_err(a.softmax, score_of(z_s[next_e]), next_c, dz);
+            has = true;
+        }
+        open |= has && my_c - nc <= my_u + nu;
+    }
+    open = __any_sync(full, open) && !__any_sync(full, odd);
+    if (open) {
+        double p;
+        __syncwarp();
+        route_exact(a, kBf16, t, z_s, zd, pd, st, (double)dz, my_e, p);
+        my_s = (float)p;
+    }
+    float sum = 0.f;
+    for (int j = 0; j < a.k; ++j) sum += __shfl_sync(full, my_s, j);
+    if (lane < a.k) {
+        a.idx[(size_t)t * a.k + lane] = my_e;
+        a.w[(size_t)t * a.k + lane] = a.renorm ? a.scale * my_s / sum : a.scale * my_s;
+    }
+}
+
+}  // namespace coli
