@@ -1,6 +1,7 @@
 // coli_route.cu -- host side of the general router (coli_router_forward).
 #include <algorithm>
 #include <cmath>
+#include <mutex>
 
 #include "coli_host.h"
 #include "coli_route.cuh"
@@ -46,22 +47,46 @@ struct RoutePlan {
     int splits;  // pieces of K, summed by the selection kernel in order
     int chunk;   // K values of a piece
     int Ep;
-    size_t bytes;  // workspace
+    bool batch;      // the tensor-core score kernel
+    int ET, EG, n_eg, m_tiles, e_tiles;
+    int n_ctas;
+    size_t status_off, bytes;  // workspace: status word, partial scores, the score kernel's status words
 };
+
+// Batches from this size on take the tensor-core score kernel.
+constexpr int kRouteBatchMin = 9;
 
 RoutePlan route_plan(int T, int H, int E)
 {
     RoutePlan p{};
     p.Ep = (E + 3) & ~3;
-    p.mt = T >= 8 ? 8 : T >= 4 ? 4 : T >= 2 ? 2 : 1;
-    // enough pieces that a call of few tokens has about 14 warps on every SM,
-    // each at least 128 lanes' worth of 16-byte loads long
-    const long long units = (long long)E * std::max(1, (T + p.mt - 1) / p.mt);
-    const int most = std::max(1, std::min(8, (H + 127) / 128));
-    p.splits = (int)std::max(1ll, std::min((long long)most, (14ll * kRouteSms + units - 1) / units));
-    p.chunk = ((H + p.splits - 1) / p.splits + 127) / 128 * 128;
-    p.splits = (H + p.chunk - 1) / p.chunk;
-    p.bytes = kStatusBytes + align_up((size_t)p.splits * T * p.Ep * 4, 256);
+    p.batch = T >= kRouteBatchMin;
+    if (p.batch) {
+        p.m_tiles = (T + kRgM - 1) / kRgM;
+        p.e_tiles = (E + kRgMaxE - 1) / kRgMaxE;
+        p.ET = ((E + p.e_tiles - 1) / p.e_tiles + 15) / 16 * 16;
+        p.n_eg = p.ET <= 80 ? 1 : 2;  // an MMA takes at most 256 columns: 3 parts of 80 experts
+        p.EG = p.n_eg == 1 ? p.ET : (p.ET + 31) / 32 * 16;
+        p.ET = p.n_eg * p.EG;
+        p.e_tiles = (E + p.ET - 1) / p.ET;
+        const int ksteps = (H + kRgK - 1) / kRgK, tiles = p.m_tiles * p.e_tiles;
+        p.splits = std::max(1, std::min({ksteps, kRouteMaxSplits, kRouteSms / tiles}));
+        const int per = (ksteps + p.splits - 1) / p.splits;
+        p.chunk = per * kRgK;
+        p.splits = (ksteps + per - 1) / per;
+        p.n_ctas = tiles * p.splits;
+    } else {
+        p.mt = T >= 8 ? 8 : T >= 4 ? 4 : T >= 2 ? 2 : 1;
+        // enough pieces that a call of few tokens has about 14 warps on every SM,
+        // each at least 128 lanes' worth of 16-byte loads long
+        const long long units = (long long)E * std::max(1, (T + p.mt - 1) / p.mt);
+        const int most = std::max(1, std::min(8, (H + 127) / 128));
+        p.splits = (int)std::max(1ll, std::min((long long)most, (14ll * kRouteSms + units - 1) / units));
+        p.chunk = ((H + p.splits - 1) / p.splits + 127) / 128 * 128;
+        p.splits = (H + p.chunk - 1) / p.chunk;
+    }
+    p.status_off = kStatusBytes + align_up((size_t)p.splits * T * p.Ep * 4, 256);
+    p.bytes = p.status_off + align_up((size_t)p.n_ctas * 4, 256);
     return p;
 }
 
@@ -75,6 +100,35 @@ cudaError_t launch_rows(const RouteArgs& a, int mt, cudaStream_t s)
         case 4: route_rows_kernel<4, kBf16><<<grid, kRouteThreads, 0, s>>>(a); break;
         default: route_rows_kernel<8, kBf16><<<grid, kRouteThreads, 0, s>>>(a); break;
     }
+    return cudaGetLastError();
+}
+
+// The batch kernel's shared memory is allowed once per device.
+std::mutex g_allow_mu;
+bool g_allowed[64];
+
+coli_status allow_batch_kernels()
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    if (dev < 0 || dev >= 64) return fail(COLI_ERR_UNSUPPORTED, "device %d out of range", dev);
+    std::lock_guard<std::mutex> lock(g_allow_mu);
+    if (g_allowed[dev]) return COLI_OK;
+    if ((e = cudaFuncSetAttribute(route_gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  (int)RgShape<true>::kSmem)) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(route_gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  (int)RgShape<false>::kSmem)) != cudaSuccess)
+        return cuda_fail(e, "kernel attribute setup");
+    g_allowed[dev] = true;
+    return COLI_OK;
+}
+
+template <bool kBf16>
+cudaError_t launch_batch(const RouteArgs& a, const RoutePlan& p, cudaStream_t s)
+{
+    const RgArgs g{p.ET, p.EG, p.n_eg, wait_limit(kRgWaitNs)};
+    route_gemm_kernel<kBf16><<<dim3(p.m_tiles, p.e_tiles, p.splits), kRgThreads, RgShape<kBf16>::kSmem, s>>>(a, g);
     return cudaGetLastError();
 }
 
@@ -133,7 +187,15 @@ coli_status coli_router_forward(const coli_router* r, const void* x, coli_dtype 
     a.splits = p.splits, a.Ep = p.Ep, a.chunk = p.chunk;
     a.idx = topk_idx, a.w = topk_w;
     const bool bf16 = xt == COLI_BF16;
-    cudaError_t e = bf16 ? launch_rows<true>(a, p.mt, stream) : launch_rows<false>(a, p.mt, stream);
+    a.cta_status = reinterpret_cast<int*>(static_cast<char*>(workspace) + p.status_off);
+    a.n_ctas = p.n_ctas;
+    cudaError_t e;
+    if (p.batch) {
+        if ((st = allow_batch_kernels()) != COLI_OK) return st;
+        e = bf16 ? launch_batch<true>(a, p, stream) : launch_batch<false>(a, p, stream);
+    } else {
+        e = bf16 ? launch_rows<true>(a, p.mt, stream) : launch_rows<false>(a, p.mt, stream);
+    }
     if (e != cudaSuccess) return cuda_fail(e, "router score launch");
     e = bf16 ? launch_select<true>(a, stream) : launch_select<false>(a, stream);
     return e == cudaSuccess ? COLI_OK : cuda_fail(e, "router selection launch");

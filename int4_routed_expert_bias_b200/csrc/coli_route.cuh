@@ -19,6 +19,7 @@
 #pragma once
 
 #include "coli_common.cuh"
+#include "coli_tcgen05.cuh"
 
 namespace coli {
 
@@ -42,6 +43,8 @@ struct RouteArgs {
     const float* w_router;   // [E, H]
     const float* bias;       // [E] or null
     int* status;             // the call's status word
+    int* cta_status;         // [n_ctas] of the batch score kernel (n_ctas == 0: the row kernel ran)
+    int n_ctas;
     float* part;             // [splits, T, Ep] partial scores
     int splits, Ep;          // Ep: E rounded up to a multiple of 4
     int chunk;               // K values of one split
@@ -98,6 +101,234 @@ __global__ void __launch_bounds__(kRouteThreads) route_rows_kernel(const __grid_
     for (int t = 0; t < MT; ++t) {
         const float v = warp_sum(acc[t]);
         if (lane == 0 && t < nt) a.part[((size_t)sp * a.T + t0 + t) * a.Ep + e] = v;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Scores, batch form: tensor cores.  Z[128 tokens, ET experts] += X . W^T over
+// one piece of K per CTA.  fp32 operands go in as sums of bf16 numbers: cutting
+// an fp32 value after its top 16 bits gives a bf16 number, the rest is exact in
+// fp32 and is cut again, so v = v0 + v1 + v2 exactly, each |v(i+1)| < 2^-7 |v(i)|
+// (8 significant bits at a time).  A bf16 activation is its own first part.
+// The products x_i w_j with i + j <= 2 are kept; what is dropped is below
+// 2^-21 of |x||w| (bf16 activations drop nothing).
+//
+// The parts of W lie one behind another along the MMA's N: one tcgen05.mma over
+// N = 3 EG columns multiplies a part of x with all parts of EG experts, and the
+// accumulator's three column groups collect orders 0, 1 and 2 (part i of x
+// starts at column group i with 3 - i parts of W).  So x is read from shared
+// memory once for three products, and small terms are not added to large sums
+// until the epilogue.
+//
+// Sixteen producer warps in two halves, alternate 64-K steps: global loads of
+// the next step in registers, split, 128-byte-swizzled stores; one thread issues
+// the MMAs; the producers then read the accumulators back.  The split costs about
+// as many issue slots as the MMAs cost tensor time, and W is split once per 128
+// tokens, so the pieces of K are as few as fill the SMs once.
+constexpr int kRgM = 128, kRgK = 64;
+constexpr int kRgHalf = 256;                   // producer threads of one half
+constexpr int kRgProducers = 2 * kRgHalf;
+constexpr int kRgThreads = kRgProducers + 32;  // and the MMA warp
+constexpr int kRgMaxE = 128;                   // experts per CTA
+constexpr int kRgPlaneA = kRgM * 128;          // bytes of one part of x in a stage
+constexpr int kRgTmemCols = 512;
+constexpr unsigned long long kRgWaitNs = 2000000000ull;  // 2 s: far beyond any legitimate wait
+constexpr unsigned long long kRgDrainNs = 100000000ull;  // teardown waits
+
+template <bool kBf16>
+struct RgShape {
+    static constexpr int kPartsX = kBf16 ? 1 : 3;
+    static constexpr int kStages = kBf16 ? 3 : 2;
+    static constexpr int kStageBytes = kPartsX * kRgPlaneA + 3 * kRgMaxE * 128;
+    static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes;
+};
+
+struct RgArgs {
+    int ET;       // experts of a CTA (multiple of 16, <= 128)
+    int EG;       // experts of one MMA (multiple of 16, <= 80); ET = n_eg * EG
+    int n_eg;
+    unsigned long long wait_ns;
+};
+
+// Eight fp32 values -> eight bf16 of part 0, 1, 2 (16 bytes each), exact.
+__device__ __forceinline__ void split8(const float (&v)[8], uint4 (&o)[3])
+{
+    float r[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[j] = v[j];
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            w[j] = __byte_perm(__float_as_uint(r[2 * j]), __float_as_uint(r[2 * j + 1]), 0x7632);
+        o[p] = make_uint4(w[0], w[1], w[2], w[3]);
+        if (p < 2) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) r[j] -= __uint_as_float(__float_as_uint(r[j]) & 0xFFFF0000u);
+        }
+    }
+}
+
+template <bool kBf16>
+__global__ void __launch_bounds__(kRgThreads, 1)
+route_gemm_kernel(const __grid_constant__ RouteArgs a, const __grid_constant__ RgArgs g)
+{
+    using S = RgShape<kBf16>;
+    extern __shared__ __align__(16) unsigned char rg_smem_raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>(
+        (reinterpret_cast<uintptr_t>(rg_smem_raw) + 1023) & ~(uintptr_t)1023);
+    __shared__ uint64_t full[S::kStages], empty[S::kStages], done;
+    __shared__ uint32_t tmem_base;
+    __shared__ int status;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int m0 = blockIdx.x * kRgM, e0 = blockIdx.y * g.ET;
+    const int k0 = blockIdx.z * a.chunk;
+    const int k1 = min(a.H, k0 + a.chunk);
+    const int steps = (k1 - k0 + kRgK - 1) / kRgK;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(&full[i], kRgHalf / 32);  // one arrival per producer warp of a half
+            mbar_init(&empty[i], 1);
+        }
+        mbar_init(&done, 1);
+        status = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kRgProducers / 32) tmem_alloc(&tmem_base, kRgTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base;
+    const unsigned long long deadline = global_ns() + g.wait_ns;
+
+    if (warp < kRgProducers / 32) {
+        const int half = warp >> 3, tid = threadIdx.x & (kRgHalf - 1);
+        // 16-byte chunks (8 values) of a step: row id >> 3, chunk id & 7, id = tid + 256 q
+        const int c8 = tid & 7, r0 = tid >> 3;
+        constexpr int kQ = kRgM * 8 / kRgHalf;  // 4
+        float wv[kQ][8];
+        float xv[kBf16 ? 1 : kQ][8];
+        uint4 xb[kBf16 ? kQ : 1];
+        auto load = [&](int j) {
+            const int k = k0 + j * kRgK + 8 * c8;
+            const bool kin = k < k1;
+#pragma unroll
+            for (int q = 0; q < kQ; ++q) {
+                const int r = r0 + 32 * q;
+                float4 w0 = make_float4(0.f, 0.f, 0.f, 0.f), w1 = w0;
+                if (kin && r < g.ET && e0 + r < a.E) {
+                    const float4* p = reinterpret_cast<const float4*>(a.w_router + (size_t)(e0 + r) * a.H + k);
+                    w0 = p[0], w1 = p[1];
+                }
+                wv[q][0] = w0.x, wv[q][1] = w0.y, wv[q][2] = w0.z, wv[q][3] = w0.w;
+                wv[q][4] = w1.x, wv[q][5] = w1.y, wv[q][6] = w1.z, wv[q][7] = w1.w;
+                const bool in = kin && m0 + r < a.T;
+                if constexpr (kBf16) {
+                    xb[q] = in ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + (size_t)(m0 + r) * a.H + k)
+                               : make_uint4(0u, 0u, 0u, 0u);
+                } else {
+                    float4 x0 = make_float4(0.f, 0.f, 0.f, 0.f), x1 = x0;
+                    if (in) {
+                        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.x) + (size_t)(m0 + r) * a.H + k);
+                        x0 = p[0], x1 = p[1];
+                    }
+                    xv[q][0] = x0.x, xv[q][1] = x0.y, xv[q][2] = x0.z, xv[q][3] = x0.w;
+                    xv[q][4] = x1.x, xv[q][5] = x1.y, xv[q][6] = x1.z, xv[q][7] = x1.w;
+                }
+            }
+        };
+        if (half < steps) load(half);
+        for (int j = half; j < steps; j += 2) {
+            const int s = j % S::kStages;
+            bool ok = true;
+            if (j >= S::kStages) ok = mbar_wait(&empty[s], ((j / S::kStages) - 1) & 1, deadline, &status);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            unsigned char* st = smem + (size_t)s * S::kStageBytes;
+            unsigned char* stw = st + S::kPartsX * kRgPlaneA;
+#pragma unroll
+            for (int q = 0; q < kQ; ++q) {
+                const int r = r0 + 32 * q;
+                uint4 o[3];
+                if constexpr (kBf16) {
+                    *reinterpret_cast<uint4*>(st + r * 128 + ((c8 ^ (r & 7)) << 4)) = xb[q];
+                } else {
+                    split8(xv[q], o);
+#pragma unroll
+                    for (int p = 0; p < 3; ++p)
+                        *reinterpret_cast<uint4*>(st + p * kRgPlaneA + r * 128 + ((c8 ^ (r & 7)) << 4)) = o[p];
+                }
+                if (r < g.ET) {
+                    const int eg = r >= g.EG ? 1 : 0;  // at most two expert groups
+                    split8(wv[q], o);
+#pragma unroll
+                    for (int p = 0; p < 3; ++p) {
+                        const int row = (eg * 3 + p) * g.EG + (r - eg * g.EG);
+                        *reinterpret_cast<uint4*>(stw + row * 128 + ((c8 ^ (row & 7)) << 4)) = o[p];
+                    }
+                }
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[s]);
+            if (j + 2 < steps) load(j + 2);
+        }
+    } else if (lane == 0) {
+        bool ok = true;
+        for (int j = 0; j < steps && ok; ++j) {
+            const int s = j % S::kStages;
+            ok = mbar_wait(&full[s], (j / S::kStages) & 1, deadline, &status);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t xs = smem_u32(smem + (size_t)s * S::kStageBytes), ws = xs + S::kPartsX * kRgPlaneA;
+#pragma unroll
+            for (int kk = 0; kk < kRgK / 16; ++kk) {
+                for (int eg = 0; eg < g.n_eg; ++eg) {
+                    const uint64_t bd = smem_desc_sw128(ws + (uint32_t)(eg * 3 * g.EG * 128) + kk * 32);
+#pragma unroll
+                    for (int p = 0; p < S::kPartsX; ++p)
+                        tc_mma_ss(tmem + (uint32_t)((eg * 3 + p) * g.EG), smem_desc_sw128(xs + p * kRgPlaneA + kk * 32), bd,
+                                  idesc_bf16((3 - p) * g.EG), p > 0 || (j | kk) != 0);
+                }
+            }
+            tc_commit(&empty[s]);
+        }
+        tc_commit(&done);  // every MMA issued above completes before the accumulators are read
+    }
+    if (warp < kRgProducers / 32) {
+        const bool ok = mbar_wait(&done, 0, deadline, &status);
+        if (__all_sync(0xFFFFFFFFu, ok)) {
+            tc_fence_after();
+            const int qd = warp & 3, t = m0 + qd * 32 + lane;
+            float* out = a.part + ((size_t)blockIdx.z * a.T + t) * a.Ep + e0;
+            const int nb = g.ET / 16, per = g.EG / 16;
+            for (int b = warp >> 2; b < nb; b += 4) {
+                const int eg = b / per, c = (b - eg * per) * 16;
+                const uint32_t col = tmem + ((uint32_t)(qd * 32) << 16) + (uint32_t)(eg * 3 * g.EG + c);
+                float v0[16], v1[16], v2[16];
+                tmem_ld16(col, v0);
+                tmem_ld16(col + g.EG, v1);
+                tmem_ld16(col + 2 * g.EG, v2);
+                if (t < a.T) {
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4)
+                        if (e0 + 16 * b + i < a.Ep)
+                            *reinterpret_cast<float4*>(out + 16 * b + i) =
+                                make_float4(v0[i] + (v1[i] + v2[i]), v0[i + 1] + (v1[i + 1] + v2[i + 1]),
+                                            v0[i + 2] + (v1[i + 2] + v2[i + 2]), v0[i + 3] + (v1[i + 3] + v2[i + 3]));
+                }
+            }
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) a.cta_status[(blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x] = status;
+    if (warp == kRgProducers / 32) {
+        if (lane == 0) mbar_wait(&done, 0, global_ns() + kRgDrainNs, &status);
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, kRgTmemCols);
     }
 }
 
@@ -389,7 +620,14 @@ __global__ void __launch_bounds__(kRouteThreads) route_select_kernel(const __gri
     const int E = a.E, t0 = blockIdx.x * tokens, nt = min(tokens, a.T - t0);
     const size_t stride = route_token_smem(E);
     griddep_wait();
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
+    if (blockIdx.x == 0) {  // the call's status word: the largest of the score kernel's CTAs
+        if (warp == 0) {
+            int bad = 0;
+            for (int i = lane; i < a.n_ctas; i += 32) bad |= a.cta_status[i];
+            if (__any_sync(full, bad != 0)) bad = 1;
+            if (lane == 0) *a.status = bad;
+        }
+    }
     {
         const int Ep = a.Ep, Eq = Ep / 4;
         const size_t plane = (size_t)a.T * Ep;
