@@ -153,12 +153,24 @@ SCORES = {"sigmoid": 0, "softmax": 1}
 
 def _check_tensor(t, name, shape, dtypes):
     """Refuse a tensor the C calls would misread: they take bare pointers."""
+    if t.shape == shape and t.dtype in dtypes and t.is_contiguous():
+        return
     if tuple(t.shape) != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} is not contiguous")
+    raise ValueError(f"{name} is not contiguous")
+
+
+def _stream_of(t, stream):
+    """The stream of a call on tensor t: the given one, else the current one.  The
+    C calls launch on the current device, so a tensor on another GPU is refused."""
+    import torch
+    if t.is_cuda and t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 class Router:
@@ -195,8 +207,8 @@ def router_forward(router, x, topk_idx, topk_w, workspace, stream=None):
     _check_tensor(x, "x", (T, router.hidden), (torch.bfloat16, torch.float32))
     _check_tensor(topk_idx, "topk_idx", (T, router.top_k), (torch.int32,))
     _check_tensor(topk_w, "topk_w", (T, router.top_k), (torch.float32,))
-    _check(_lib.coli_router_forward(router.ref, _ptr(x), _dtype_code(x), T, _ptr(topk_idx), _ptr(topk_w),
-                                    _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+    _check(_lib.coli_router_forward(router.ref, x.data_ptr(), _dtype_code(x), T, topk_idx.data_ptr(), topk_w.data_ptr(),
+                                    workspace.data_ptr(), workspace.nbytes, _stream_of(x, stream)))
 
 
 def expert_union(topk_idx, E, count, offset, active, n_active, perm, inv_perm, stream=None):

@@ -187,6 +187,11 @@ coli_status coli_router_forward(const coli_router* r, const void* x, coli_dtype 
     a.splits = p.splits, a.Ep = p.Ep, a.chunk = p.chunk;
     a.idx = topk_idx, a.w = topk_w;
     const bool bf16 = xt == COLI_BF16;
+    a.gmul = (uint32_t)(((1u << 20) + r->n_experts / a.groups - 1) / (r->n_experts / a.groups));
+    // Largest error seen against double sums over random and trained-like inputs, relative to the token's
+    // largest |z|: 2^-22.5 for the row kernel (short fp32 chains); the tensor core drops what does not fit its
+    // fp32 accumulator at each of the chunk / 16 accumulations, 2^-24.9 each.  Four times that and more is allowed for.
+    a.sum_err = p.batch ? 0x1p-20f + 0x1p-23f * (float)(p.chunk / 16) : 0x1p-20f;
     a.cta_status = reinterpret_cast<int*>(static_cast<char*>(workspace) + p.status_off);
     a.n_ctas = p.n_ctas;
     cudaError_t e;

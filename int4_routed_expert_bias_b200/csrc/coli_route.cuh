@@ -14,8 +14,8 @@
 // experts, the last selected against the first rejected one, the last eligible
 // group against the first rejected one) is checked against the largest error
 // those sums can carry, and where one is closer than that the experts concerned
-// are summed again in double, until all decisions are clear (route_exact).
-// That is rare and touches a few rows of x and W that are in L2.
+// are summed again in double (route_close; route_exact for what that leaves
+// open).  It touches a few rows of x and W that are in L2.
 #pragma once
 
 #include "coli_common.cuh"
@@ -29,9 +29,6 @@ constexpr int kRouteMaxGroups = 32;
 constexpr int kRouteSms = 148;      // grid sizing (B200); the results do not depend on it
 constexpr int kRouteRowsMT = 8;     // tokens per pass of the row kernel
 constexpr int kRouteMaxSplits = 64;
-
-// Error of an fp32 score sum that the selection allows for, relative to the token's largest |z|.
-constexpr float kRouteSumErr = 1.0f / 131072.0f;  // 2^-17
 
 struct RouteArgs {
     int T, H, E, k;
@@ -48,6 +45,8 @@ struct RouteArgs {
     float* part;             // [splits, T, Ep] partial scores
     int splits, Ep;          // Ep: E rounded up to a multiple of 4
     int chunk;               // K values of one split
+    float sum_err;           // error of an fp32 score that the selection allows for, relative to the token's largest |z|
+    uint32_t gmul;           // ceil(2^20 / experts per group): e / m = e * gmul >> 20 for e < 1024
     int32_t* idx;            // [T, k]
     float* w;                // [T, k]
 };
@@ -371,7 +370,7 @@ __device__ __forceinline__ double route_dot(const RouteArgs& a, bool bf16, int t
     const float* wrow = a.w_router + (size_t)e * a.H;
     const char* xr = static_cast<const char*>(a.x) + (size_t)t * a.H * (bf16 ? 2 : 4);
     double s0 = 0., s1 = 0., s2 = 0., s3 = 0.;
-#pragma unroll 4
+#pragma unroll 8
     for (int i = lane * 4; i < a.H; i += 128) {
         const float4 w = *reinterpret_cast<const float4*>(wrow + i);
         const float4 v = bf16 ? load_act4<true>(xr, i) : load_act4<false>(xr, i);
@@ -599,9 +598,140 @@ __device__ __noinline__ void route_exact(const RouteArgs& a, bool bf16, int t, c
     }
 }
 
+// Double-precision value that the choice score of expert e is ordered by, from
+// its exact z: sigmoid + bias, or the softmax numerator over the fp32
+// denominator (a factor common to all experts) + bias.  p: the part without bias.
+__device__ __forceinline__ double choice_exact(const RouteArgs& a, int e, double z, float zm, float den, double& p)
+{
+    p = a.softmax ? exp(z - (double)zm) / (double)den : 1. / (1. + exp(-z));
+    return a.bias ? p + (double)a.bias[e] : p;
+}
+
+// What the selection knows of a token's groups, lane g < G holding group g.
+struct GroupState {
+    float score, last;  // its score; the smallest choice score counted in it
+    float lo, hi;       // smallest score of a kept group, largest of a rejected one
+    float err;          // bound on the error of any group's score
+    uint32_t kept;      // bit per group
+};
+
+// The selection of one token with a few open decisions, by one warp: the border
+// groups' leading experts are summed in double and the border drawn again; then
+// the ranking in fp32 is carried on past k until a clear gap, and every run of
+// neighbours without a clear gap is ordered by double sums.  Lane j < k returns
+// slot j.  false: too many open decisions, or the softmax denominator's own
+// error matters (route_exact takes those).
+__device__ __noinline__ bool route_close(const RouteArgs& a, bool bf16, int t, const float* z_s, const float* c_s, float dz,
+                                         float zm, float den, GroupState gs, int& my_e, double& my_p)
+{
+    const int lane = threadIdx.x & 31;
+    const unsigned full = 0xFFFFFFFFu;
+    const int E = a.E, G = a.groups, m = E / G;
+    const double dd = a.softmax && a.bias ? (double)dz + 0x1p-20 : 0.;  // relative error of the denominator
+    auto at = [&](int e) { return G > 1 ? e + (int)(e * a.gmul >> 20) : e; };
+    if (G > 1 && gs.lo - gs.hi <= 2.f * gs.err) {
+        const bool in = lane < G && ((gs.kept >> lane) & 1u);
+        const bool open = lane < G && (in ? gs.score - gs.hi <= 2.f * gs.err : gs.lo - gs.score <= 2.f * gs.err);
+        const uint32_t border = __ballot_sync(full, open);
+        double sc = 0., sp = 0.;  // lane g: the score of a border group, and its part without biases
+        for (uint32_t left = border; left; left &= left - 1) {
+            const int g = __ffs(left) - 1;
+            const float floor_c = __shfl_sync(full, gs.last, g) - 2.f * gs.err;
+            double v1 = -INFINITY, v2 = -INFINITY, p1 = 0., p2 = 0.;
+            for (int b = g * m; b < (g + 1) * m; b += 32) {
+                uint32_t cand = __ballot_sync(full, b + lane < (g + 1) * m && c_s[at(b + lane)] >= floor_c);
+                for (; cand; cand &= cand - 1) {
+                    const int e = b + __ffs(cand) - 1;
+                    double p;
+                    const double v = choice_exact(a, e, route_dot(a, bf16, t, e), zm, den, p);
+                    if (v > v1) v2 = v1, p2 = p1, v1 = v, p1 = p;
+                    else if (v > v2) v2 = v, p2 = p;
+                }
+            }
+            if (lane == g) sc = a.top == 2 ? v1 + v2 : v1, sp = a.top == 2 ? p1 + p2 : p1;
+        }
+        const int slots = a.keep - __popc(gs.kept & ~border);
+        int rank = 0;
+        for (uint32_t left = border; left; left &= left - 1) {
+            const int g = __ffs(left) - 1;
+            const double o = __shfl_sync(full, sc, g);
+            rank += (o > sc || (o == sc && g < lane)) ? 1 : 0;
+        }
+        const uint32_t chosen = __ballot_sync(full, open && rank < slots);
+        bool close = false;
+        for (uint32_t left = border; left; left &= left - 1) {
+            const int g = __ffs(left) - 1;
+            const double o = __shfl_sync(full, sc, g), op = __shfl_sync(full, sp, g);
+            close |= open && ((chosen >> g) & 1u) != ((chosen >> lane) & 1u) && fabs(o - sc) < dd * fabs(op - sp);
+        }
+        if (__any_sync(full, close)) return false;
+        gs.kept = (gs.kept & ~border) | chosen;
+    }
+    // fp32 ranking until a clear gap behind slot k
+    float my_c = 0.f, my_u = 0.f, prev_c = INFINITY;
+    int prev_e = -1, n = 0;
+    my_e = 0;
+    const int most = min(32, G > 1 ? a.keep * m : E);
+    for (; n < most; ++n) {
+        float bc = -INFINITY;
+        int be = 1 << 20;
+        for (int e = lane; e < E; e += 32) {
+            if (G > 1 && !((gs.kept >> (e * a.gmul >> 20)) & 1u)) continue;
+            const float c = c_s[at(e)];
+            if (!(c < prev_c || (c == prev_c && e > prev_e))) continue;  // taken
+            if (be == 1 << 20 || c > bc) bc = c, be = e;
+        }
+        const uint32_t key = be == 1 << 20 ? 0u : order_key(bc);
+        const uint32_t top = __reduce_max_sync(full, key);
+        const int e = (int)__reduce_min_sync(full, key == top ? (uint32_t)be : 0xFFFFFFFFu);
+        const float c = order_value(top);
+        const float s = a.softmax ? expf(z_s[e] - zm) / den : 1.0f / (1.0f + expf(-z_s[e]));
+        const float u = choice_err(a.softmax, s, c, dz);
+        if (lane == n) my_e = e, my_c = c, my_u = u, my_p = (double)s;
+        const float last_u = __shfl_sync(full, my_u, n > 0 ? n - 1 : 0);
+        if (n >= a.k && !(prev_c - c <= last_u + u)) break;  // slot k is clear of everything behind
+        prev_c = c, prev_e = e;
+    }
+    if (n == 32 && n < (G > 1 ? a.keep * m : E)) return false;
+    const float nc = __shfl_down_sync(full, my_c, 1), nu = __shfl_down_sync(full, my_u, 1);
+    const uint32_t open = __ballot_sync(full, lane + 1 < n && my_c - nc <= my_u + nu);
+    double v = (double)my_c;
+    for (uint32_t left = open | (open << 1); left; left &= left - 1) {
+        const int j = __ffs(left) - 1;
+        const int e = __shfl_sync(full, my_e, j);
+        const double z = route_dot(a, bf16, t, e);
+        double p;
+        const double w = choice_exact(a, e, z, zm, den, p);
+        if (lane == j) v = w, my_p = p;
+    }
+    // slot of each: runs stay in place, inside a run by the double sums (equal: lower expert first)
+    const int run = __popc(~open & ((1u << lane) - 1u));
+    int slot = 0;
+    bool close = false;
+    for (int i = 0; i < n; ++i) {
+        const double o = __shfl_sync(full, v, i), op = __shfl_sync(full, my_p, i);
+        const int oe = __shfl_sync(full, my_e, i), orun = __shfl_sync(full, run, i);
+        if (orun == run) {
+            slot += (o > v || (o == v && oe < my_e)) ? 1 : 0;
+            close |= lane < n && i != lane && fabs(o - v) < dd * fabs(op - my_p);
+        } else {
+            slot += i < lane ? 1 : 0;
+        }
+    }
+    if (__any_sync(full, close)) return false;
+    int src = lane;
+    for (int i = 0; i < n; ++i) {
+        const int o = __shfl_sync(full, slot, i);
+        if (o == lane) src = i;
+    }
+    my_e = __shfl_sync(full, my_e, src);
+    my_p = __shfl_sync(full, my_p, src);
+    return true;
+}
+
 // Shared memory of one token of the selection kernel: z [E] floats, then zd [E]
 // and pd [E] doubles (pd's place holds the fp32 choice scores, padded by one
-// per group, on the usual path), then a state byte per expert.
+// per group, until route_exact), then a state byte per expert.
 __host__ __device__ __forceinline__ size_t route_token_smem(int E)
 {
     const size_t pd = (size_t)E * 8 > (size_t)E * 4 + 128 ? (size_t)E * 8 : (size_t)E * 4 + 128;
@@ -619,14 +749,15 @@ __global__ void __launch_bounds__(kRouteThreads) route_select_kernel(const __gri
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int E = a.E, t0 = blockIdx.x * tokens, nt = min(tokens, a.T - t0);
     const size_t stride = route_token_smem(E);
+    float bias[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) bias[i] = a.bias && lane + 32 * i < E ? a.bias[lane + 32 * i] : 0.f;
     griddep_wait();
-    if (blockIdx.x == 0) {  // the call's status word: the largest of the score kernel's CTAs
-        if (warp == 0) {
-            int bad = 0;
-            for (int i = lane; i < a.n_ctas; i += 32) bad |= a.cta_status[i];
-            if (__any_sync(full, bad != 0)) bad = 1;
-            if (lane == 0) *a.status = bad;
-        }
+    if (blockIdx.x == 0 && warp == kRouteWarps - 1) {  // the call's status word, from the score kernel's CTAs
+        int bad = 0;
+        for (int i = lane; i < a.n_ctas; i += 32) bad |= a.cta_status[i];
+        bad = __any_sync(full, bad != 0) ? 1 : 0;
+        if (lane == 0) *a.status = bad;
     }
     {
         const int Ep = a.Ep, Eq = Ep / 4;
@@ -658,65 +789,63 @@ __global__ void __launch_bounds__(kRouteThreads) route_select_kernel(const __gri
     const float* z_s = reinterpret_cast<const float*>(base);
     double* zd = reinterpret_cast<double*>(base + align_up((size_t)E * 4, 16));
     double* pd = zd + align_up((size_t)E * 8, 16) / 8;
+    float* c_s = reinterpret_cast<float*>(pd);
     unsigned char* st = base + stride - align_up((size_t)E, 16);
 
-    float z[kPer], c[kPer];
+    float c[kPer];
     float zmax = 0.f, zm = -INFINITY;
     bool odd = false;  // a score that is not finite
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int e = lane + 32 * i;
-        z[i] = e < E ? z_s[e] : 0.f;
-        zmax = fmaxf(zmax, fabsf(z[i]));
-        odd |= !(fabsf(z[i]) < INFINITY);
-        if (e < E) zm = fmaxf(zm, z[i]);
+        c[i] = e < E ? z_s[e] : 0.f;
+        zmax = fmaxf(zmax, fabsf(c[i]));
+        odd |= !(fabsf(c[i]) < INFINITY);
+        if (e < E) zm = fmaxf(zm, c[i]);
     }
     zmax = warp_max(zmax);
-    zm = warp_max(zm);
-    const float dz = kRouteSumErr * zmax;
+    const float dz = a.sum_err * zmax;
     // s_e: the unbiased score
     float den = 1.f;
     if (a.softmax) {
+        zm = warp_max(zm);
         float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (lane + 32 * i < E) sum += expf(z[i] - zm);
+        for (int i = 0; i < kPer; ++i) {
+            c[i] = lane + 32 * i < E ? expf(c[i] - zm) : 0.f;
+            sum += c[i];
+        }
         den = warp_sum(sum);
     }
     auto score_of = [&](float v) { return a.softmax ? expf(v - zm) / den : 1.0f / (1.0f + expf(-v)); };
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const int e = lane + 32 * i;
-        c[i] = -INFINITY;
-        if (e < E) {
-            const float s = score_of(z[i]);
-            const float v = a.bias ? s + a.bias[e] : s;
-            c[i] = v == v ? v : -INFINITY;  // NaN ranks last: the order stays total
-        }
+        const float s = a.softmax ? c[i] / den : 1.0f / (1.0f + expf(-c[i]));
+        const float v = s + bias[i];
+        c[i] = v == v ? v : -INFINITY;  // NaN ranks last: the order stays total
     }
 
     // eligible groups
-    uint32_t kept = full;
+    uint32_t kept = full;  // bit per group
     bool open = false;
     const int G = a.groups, m = E / G;
+    GroupState gs{0.f, 0.f, 0.f, 0.f, 0.f, full};
     if (G > 1) {
-        float* c_s = reinterpret_cast<float*>(pd);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int e = lane + 32 * i;
-            if (e < E) c_s[e + e / m] = c[i];
+            if (e < E) c_s[e + (int)(e * a.gmul >> 20)] = c[i];
         }
         __syncwarp();
-        // 32 / 2^ceil(log2 G) lanes per group, each a strided share of its experts
-        int lg = 32;
-        while (lg > 1 && G * lg > 32) lg >>= 1;
-        const int g = lane / lg, r = lane - g * lg;
-        float b1 = -INFINITY, b2 = -INFINITY, u = 0.f;
+        // 2^floor(log2(32 / G)) lanes per group, each a strided share of its experts
+        const int lsh = 31 - __clz(32 / G), lg = 1 << lsh;
+        const int g = lane >> lsh, r = lane & (lg - 1);
+        float b1 = -INFINITY, b2 = -INFINITY;
         if (g < G) {
             for (int j = r; j < m; j += lg) {
                 const float v = c_s[g * (m + 1) + j];
-                if (v > b1) b2 = b1, b1 = v;
-                else if (v > b2) b2 = v;
+                b2 = fmaxf(b2, fminf(b1, v));
+                b1 = fmaxf(b1, v);
             }
         }
         for (int o = lg >> 1; o > 0; o >>= 1) {
@@ -725,39 +854,42 @@ __global__ void __launch_bounds__(kRouteThreads) route_select_kernel(const __gri
             b1 = fmaxf(b1, o1);
         }
         const float s_most = 1.f / den;  // no softmax score is larger
-        u = choice_err(a.softmax, s_most, b1, dz);
+        float err = choice_err(a.softmax, s_most, b1, dz);
         float score = b1;
         if (a.top == 2) {
-            u += choice_err(a.softmax, s_most, b2, dz);
+            err += choice_err(a.softmax, s_most, b2, dz);
             score = b1 + b2;
         }
         if (!(score == score)) score = -INFINITY;
+        // lane g takes over group g
+        const int from = (lane << lsh) & 31;
+        gs.score = __shfl_sync(full, score, from);
+        gs.last = __shfl_sync(full, a.top == 2 ? b2 : b1, from);
         int rank = 0;
         for (int h = 0; h < G; ++h) {
-            const float o = __shfl_sync(full, score, h * lg);
-            rank += (o > score || (o == score && h < g)) ? 1 : 0;
+            const float o = __shfl_sync(full, gs.score, h);
+            rank += (o > gs.score || (o == gs.score && h < lane)) ? 1 : 0;
         }
-        const bool in = g < G && rank < a.keep;
-        kept = 0;
-        for (int h = 0; h < G; ++h) kept |= (__shfl_sync(full, (uint32_t)in, h * lg) & 1u) << h;
-        if (a.keep < G) {
-            const float lo = warp_min(in ? score : INFINITY), hi = warp_max(g < G && !in ? score : -INFINITY);
-            const float um = warp_max(g < G ? u : 0.f);
-            open = lo - hi <= 2.f * um;
-        }
+        const bool in = lane < G && rank < a.keep;
+        kept = __ballot_sync(full, in);
+        gs.lo = warp_min(in ? gs.score : INFINITY);
+        gs.hi = warp_max(lane < G && !in ? gs.score : -INFINITY);
+        gs.err = warp_max(g < G ? err : 0.f);
+        gs.kept = kept;
+        open = gs.lo - gs.hi <= 2.f * gs.err;
     }
 
     uint32_t key[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int e = lane + 32 * i;
-        key[i] = e < E && (G == 1 || ((kept >> (e / m)) & 1u)) ? order_key(c[i]) : 0u;
+        key[i] = e < E && (G == 1 || ((kept >> (e * a.gmul >> 20)) & 1u)) ? order_key(c[i]) : 0u;
     }
     // k rounds (and one more, for the gap to the first rejected expert)
     int my_e = 0;
     float my_c = 0.f, next_c = -INFINITY;
     int next_e = -1;
-    const int rounds = a.k + (a.k < a.keep * m ? 1 : 0);
+    const int rounds = a.k + (a.k < (G > 1 ? a.keep * m : E) ? 1 : 0);
     for (int j = 0; j < rounds; ++j) {
         uint32_t best = key[0];
         int bi = 0;
@@ -790,9 +922,17 @@ __global__ void __launch_bounds__(kRouteThreads) route_select_kernel(const __gri
     }
     open = __any_sync(full, open) && !__any_sync(full, odd);
     if (open) {
-        double p;
+        double p = 0.;
+        if (G == 1) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (lane + 32 * i < E) c_s[lane + 32 * i] = c[i];
+        }
         __syncwarp();
-        route_exact(a, kBf16, t, z_s, zd, pd, st, (double)dz, my_e, p);
+        if (dz == 0.f || !route_close(a, kBf16, t, z_s, c_s, dz, zm, den, gs, my_e, p)) {
+            __syncwarp();
+            route_exact(a, kBf16, t, z_s, zd, pd, st, (double)dz, my_e, p);
+        }
         my_s = (float)p;
     }
     float sum = 0.f;
