@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
 #include <cstddef>
 #include <cstdint>
@@ -19,6 +20,15 @@ coli_status cuda_fail(cudaError_t e, const char* what);
 
 // The limit of the kernels' bounded waits: the test hook's value if set, else dflt.
 unsigned long long wait_limit(unsigned long long dflt);
+
+// cuTensorMapEncodeTiled from the CUDA driver, looked up once (the library links
+// only the runtime).  nullptr when the CUDA driver does not provide it.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+
+// Row-major 2-D tensor [rows, inner] of esize-byte elements, read in boxes of
+// box_inner x box_rows.
+bool encode_2d(CUtensorMap* m, CUtensorMapDataType dt, size_t esize, const void* base, uint64_t inner, uint64_t rows,
+               uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle sw);
 
 inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 

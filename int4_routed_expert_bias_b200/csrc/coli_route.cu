@@ -48,7 +48,7 @@ struct RoutePlan {
     int chunk;   // K values of a piece
     int Ep;
     bool batch;      // the tensor-core score kernel
-    int ET, EG, n_eg, m_tiles, e_tiles;
+    int ET, m_tiles, e_tiles;
     int n_ctas;
     size_t status_off, bytes;  // workspace: status word, partial scores, the score kernel's status words
 };
@@ -65,10 +65,6 @@ RoutePlan route_plan(int T, int H, int E)
         p.m_tiles = (T + kRgM - 1) / kRgM;
         p.e_tiles = (E + kRgMaxE - 1) / kRgMaxE;
         p.ET = ((E + p.e_tiles - 1) / p.e_tiles + 15) / 16 * 16;
-        p.n_eg = p.ET <= 80 ? 1 : 2;  // an MMA takes at most 256 columns: 3 parts of 80 experts
-        p.EG = p.n_eg == 1 ? p.ET : (p.ET + 31) / 32 * 16;
-        p.ET = p.n_eg * p.EG;
-        p.e_tiles = (E + p.ET - 1) / p.ET;
         const int ksteps = (H + kRgK - 1) / kRgK, tiles = p.m_tiles * p.e_tiles;
         p.splits = std::max(1, std::min({ksteps, kRouteMaxSplits, kRouteSms / tiles}));
         const int per = (ksteps + p.splits - 1) / p.splits;
@@ -127,8 +123,12 @@ coli_status allow_batch_kernels()
 template <bool kBf16>
 cudaError_t launch_batch(const RouteArgs& a, const RoutePlan& p, cudaStream_t s)
 {
-    const RgArgs g{p.ET, p.EG, p.n_eg, wait_limit(kRgWaitNs)};
-    route_gemm_kernel<kBf16><<<dim3(p.m_tiles, p.e_tiles, p.splits), kRgThreads, RgShape<kBf16>::kSmem, s>>>(a, g);
+    CUtensorMap tx{};
+    if (kBf16 && !encode_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.x, (uint64_t)a.H, (uint64_t)a.T, kRgK, kRgM,
+                            CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    route_gemm_kernel<kBf16><<<dim3(p.m_tiles, p.e_tiles, p.splits), kRgThreads, RgShape<kBf16>::kSmem, s>>>(
+        tx, a, p.ET, wait_limit(kRgWaitNs));
     return cudaGetLastError();
 }
 
@@ -136,8 +136,10 @@ template <bool kBf16>
 cudaError_t launch_select(const RouteArgs& a, cudaStream_t s)
 {
     const size_t per = route_token_smem(a.E);
+    // tokens per block, a power of two: one while there are SMs for it, else as many as 48 KB hold
     const int most = std::max(1, std::min(kRouteWarps, (int)(49152 / per)));
-    const int tokens = std::max(1, std::min(most, (a.T + 2 * kRouteSms - 1) / (2 * kRouteSms)));
+    int tokens = 1;
+    while (2 * tokens <= most && tokens * 2 * kRouteSms < a.T) tokens *= 2;
     const dim3 grid((a.T + tokens - 1) / tokens);
     auto go = [&](auto kern) { return launch_pdl(kern, grid, kRouteThreads, tokens * per, s, a, tokens); };
     const int n = (a.E + 31) / 32;
@@ -188,14 +190,16 @@ coli_status coli_router_forward(const coli_router* r, const void* x, coli_dtype 
     a.idx = topk_idx, a.w = topk_w;
     const bool bf16 = xt == COLI_BF16;
     a.gmul = (uint32_t)(((1u << 20) + r->n_experts / a.groups - 1) / (r->n_experts / a.groups));
-    // Largest error seen against double sums over random and trained-like inputs, relative to the token's
-    // largest |z|: 2^-22.5 for the row kernel (short fp32 chains); the tensor core drops what does not fit its
-    // fp32 accumulator at each of the chunk / 16 accumulations, 2^-24.9 each.  Four times that and more is allowed for.
-    a.sum_err = p.batch ? 0x1p-20f + 0x1p-23f * (float)(p.chunk / 16) : 0x1p-20f;
+    // Errors seen against double sums, relative to the token's largest |z|: up to 2^-22.5 for the row kernel (short
+    // fp32 chains); the tensor core drops what does not fit its fp32 accumulator at each of the 4 kRgRound
+    // accumulations that a sum runs through, up to 2^-24.9 each.  Four times that is allowed for.
+    a.sum_err = p.batch ? 0x1p-20f + 0x1p-23f * (float)std::min(p.chunk / 16, 4 * kRgRound) : 0x1p-20f;
     a.cta_status = reinterpret_cast<int*>(static_cast<char*>(workspace) + p.status_off);
     a.n_ctas = p.n_ctas;
     cudaError_t e;
     if (p.batch) {
+        if (bf16 && !tensor_map_encoder())
+            return fail(COLI_ERR_UNSUPPORTED, "the CUDA driver provides no cuTensorMapEncodeTiled (tensor-core router path)");
         if ((st = allow_batch_kernels()) != COLI_OK) return st;
         e = bf16 ? launch_batch<true>(a, p, stream) : launch_batch<false>(a, p, stream);
     } else {

@@ -112,25 +112,32 @@ __global__ void __launch_bounds__(kRouteThreads) route_rows_kernel(const __grid_
 // The products x_i w_j with i + j <= 2 are kept; what is dropped is below
 // 2^-21 of |x||w| (bf16 activations drop nothing).
 //
-// The parts of W lie one behind another along the MMA's N: one tcgen05.mma over
-// N = 3 EG columns multiplies a part of x with all parts of EG experts, and the
-// accumulator's three column groups collect orders 0, 1 and 2 (part i of x
-// starts at column group i with 3 - i parts of W).  So x is read from shared
-// memory once for three products, and small terms are not added to large sums
-// until the epilogue.
+// The parts of W lie one behind another along the MMA's N, part 0 of all ET
+// experts, then part 1, then part 2.  The accumulator has columns for order 0
+// (products of first parts) and for orders 1 and 2 side by side, so one MMA over
+// N = 2 ET multiplies a part of x with two parts of W, and small terms meet
+// large sums only in the epilogue.  The tensor core cuts what does not fit its
+// fp32 accumulator at every step (2.8e-6 of z over 192 steps, always towards
+// zero), so order 0 is collected over kRgRound steps at a time in one of two
+// column ranges, and the epilogue warps add finished ranges to the partial
+// scores in fp32 while the other range fills (measured: 2^-17.3 of the largest
+// |z| without, 2^-20 with).
 //
-// Sixteen producer warps in two halves, alternate 64-K steps: global loads of
-// the next step in registers, split, 128-byte-swizzled stores; one thread issues
-// the MMAs; the producers then read the accumulators back.  The split costs about
-// as many issue slots as the MMAs cost tensor time, and W is split once per 128
-// tokens, so the pieces of K are as few as fill the SMs once.
+// Roles: two halves of eight producer warps split fp32 operands into swizzled
+// shared memory, the next step's global loads in registers (bf16 activations:
+// the halves take alternate steps of W, TMA brings x; fp32: one half W, one x);
+// one thread issues MMAs, one TMA; four warps are the epilogue.  Bound by shared
+// memory: a 64-K step writes 64 KB and the MMAs read 80 KB, against 768 tensor
+// cycles.
 constexpr int kRgM = 128, kRgK = 64;
 constexpr int kRgHalf = 256;                   // producer threads of one half
 constexpr int kRgProducers = 2 * kRgHalf;
-constexpr int kRgThreads = kRgProducers + 32;  // and the MMA warp
+constexpr int kRgWarpEpi = kRgProducers / 32, kRgWarpMma = kRgWarpEpi + 4, kRgWarpTma = kRgWarpMma + 1;
+constexpr int kRgThreads = (kRgWarpTma + 1) * 32;
 constexpr int kRgMaxE = 128;                   // experts per CTA
+constexpr int kRgRound = 8;                    // 64-K steps that order 0 is collected over
 constexpr int kRgPlaneA = kRgM * 128;          // bytes of one part of x in a stage
-constexpr int kRgTmemCols = 512;
+constexpr int kRgTmemCols = 512, kRgO12 = 256; // columns: order 0 twice (0, 128), then orders 1 and 2
 constexpr unsigned long long kRgWaitNs = 2000000000ull;  // 2 s: far beyond any legitimate wait
 constexpr unsigned long long kRgDrainNs = 100000000ull;  // teardown waits
 
@@ -142,26 +149,16 @@ struct RgShape {
     static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes;
 };
 
-struct RgArgs {
-    int ET;       // experts of a CTA (multiple of 16, <= 128)
-    int EG;       // experts of one MMA (multiple of 16, <= 80); ET = n_eg * EG
-    int n_eg;
-    unsigned long long wait_ns;
-};
-
 // Eight fp32 values -> eight bf16 of part 0, 1, 2 (16 bytes each), exact.
-__device__ __forceinline__ void split8(const float (&v)[8], uint4 (&o)[3])
+__device__ __forceinline__ void split8(float (&r)[8], unsigned char* dst, int plane)
 {
-    float r[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) r[j] = v[j];
 #pragma unroll
     for (int p = 0; p < 3; ++p) {
         uint32_t w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             w[j] = __byte_perm(__float_as_uint(r[2 * j]), __float_as_uint(r[2 * j + 1]), 0x7632);
-        o[p] = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(dst + p * plane) = make_uint4(w[0], w[1], w[2], w[3]);
         if (p < 2) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) r[j] -= __uint_as_float(__float_as_uint(r[j]) & 0xFFFF0000u);
@@ -169,161 +166,182 @@ __device__ __forceinline__ void split8(const float (&v)[8], uint4 (&o)[3])
     }
 }
 
+// Add four floats in L2 without waiting for them.  Each place here has one adding
+// thread, whose additions to it stay in program order: the sum is deterministic.
+__device__ __forceinline__ void red_add4(float* p, float x, float y, float z, float w)
+{
+    asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
+}
+
+// tx: bf16 x [T, H], boxes of 64 x 128 tokens, 128-byte swizzle (unused for fp32 x).
+// ET: experts of a CTA, a multiple of 16, at most 128.
 template <bool kBf16>
 __global__ void __launch_bounds__(kRgThreads, 1)
-route_gemm_kernel(const __grid_constant__ RouteArgs a, const __grid_constant__ RgArgs g)
+route_gemm_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ RouteArgs a, int ET,
+                  unsigned long long wait_ns)
 {
     using S = RgShape<kBf16>;
     extern __shared__ __align__(16) unsigned char rg_smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(rg_smem_raw) + 1023) & ~(uintptr_t)1023);
-    __shared__ uint64_t full[S::kStages], empty[S::kStages], done;
+    __shared__ uint64_t full[S::kStages], empty[S::kStages], acc_full[2], acc_empty[2], done;
     __shared__ uint32_t tmem_base;
     __shared__ int status;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int m0 = blockIdx.x * kRgM, e0 = blockIdx.y * g.ET;
+    const int m0 = blockIdx.x * kRgM, e0 = blockIdx.y * ET;
     const int k0 = blockIdx.z * a.chunk;
     const int k1 = min(a.H, k0 + a.chunk);
     const int steps = (k1 - k0 + kRgK - 1) / kRgK;
+    const int rounds = (steps + kRgRound - 1) / kRgRound;
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kStages; ++i) {
-            mbar_init(&full[i], kRgHalf / 32);  // one arrival per producer warp of a half
+            mbar_init(&full[i], kBf16 ? kRgHalf / 32 + 1 : kRgProducers / 32);  // producer warps (and the TMA thread)
             mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], 4);  // one arrival per epilogue warp
         }
         mbar_init(&done, 1);
         status = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == kRgProducers / 32) tmem_alloc(&tmem_base, kRgTmemCols);
+    if (warp == kRgWarpMma) tmem_alloc(&tmem_base, kRgTmemCols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base;
-    const unsigned long long deadline = global_ns() + g.wait_ns;
+    const unsigned long long deadline = global_ns() + wait_ns;
 
-    if (warp < kRgProducers / 32) {
+    if (warp < kRgWarpEpi) {
+        // ---------------- producers ----------------
         const int half = warp >> 3, tid = threadIdx.x & (kRgHalf - 1);
-        // 16-byte chunks (8 values) of a step: row id >> 3, chunk id & 7, id = tid + 256 q
+        const bool is_x = !kBf16 && half == 1;
+        const int first = kBf16 ? half : 0, stride = kBf16 ? 2 : 1;
+        // 16-byte chunks (8 values) of a step: chunk tid & 7 of rows tid >> 3, + 32, ...
         const int c8 = tid & 7, r0 = tid >> 3;
         constexpr int kQ = kRgM * 8 / kRgHalf;  // 4
-        float wv[kQ][8];
-        float xv[kBf16 ? 1 : kQ][8];
-        uint4 xb[kBf16 ? kQ : 1];
+        const int rows = is_x ? min(kRgM, a.T - m0) : min(ET, a.E - e0);       // rows with data
+        const int height = is_x ? kRgM : ET;                                   // rows of the tile
+        const float* src = (is_x ? static_cast<const float*>(a.x) + (size_t)m0 * a.H : a.w_router + (size_t)e0 * a.H) +
+                           (size_t)r0 * a.H + k0 + 8 * c8;
+        const size_t row32 = (size_t)32 * a.H;
+        const int dst0 = (is_x ? 0 : S::kPartsX * kRgPlaneA) + r0 * 128 + ((c8 ^ (r0 & 7)) << 4);
+        const int plane = is_x ? kRgPlaneA : ET * 128;
+        float v[kQ][8];
         auto load = [&](int j) {
-            const int k = k0 + j * kRgK + 8 * c8;
-            const bool kin = k < k1;
+            const bool kin = k0 + j * kRgK + 8 * c8 < k1;
+            const float* p = src + j * kRgK;
 #pragma unroll
             for (int q = 0; q < kQ; ++q) {
-                const int r = r0 + 32 * q;
                 float4 w0 = make_float4(0.f, 0.f, 0.f, 0.f), w1 = w0;
-                if (kin && r < g.ET && e0 + r < a.E) {
-                    const float4* p = reinterpret_cast<const float4*>(a.w_router + (size_t)(e0 + r) * a.H + k);
-                    w0 = p[0], w1 = p[1];
+                if (kin && r0 + 32 * q < rows) {
+                    w0 = *reinterpret_cast<const float4*>(p + q * row32);
+                    w1 = *reinterpret_cast<const float4*>(p + q * row32 + 4);
                 }
-                wv[q][0] = w0.x, wv[q][1] = w0.y, wv[q][2] = w0.z, wv[q][3] = w0.w;
-                wv[q][4] = w1.x, wv[q][5] = w1.y, wv[q][6] = w1.z, wv[q][7] = w1.w;
-                const bool in = kin && m0 + r < a.T;
-                if constexpr (kBf16) {
-                    xb[q] = in ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + (size_t)(m0 + r) * a.H + k)
-                               : make_uint4(0u, 0u, 0u, 0u);
-                } else {
-                    float4 x0 = make_float4(0.f, 0.f, 0.f, 0.f), x1 = x0;
-                    if (in) {
-                        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.x) + (size_t)(m0 + r) * a.H + k);
-                        x0 = p[0], x1 = p[1];
-                    }
-                    xv[q][0] = x0.x, xv[q][1] = x0.y, xv[q][2] = x0.z, xv[q][3] = x0.w;
-                    xv[q][4] = x1.x, xv[q][5] = x1.y, xv[q][6] = x1.z, xv[q][7] = x1.w;
-                }
+                v[q][0] = w0.x, v[q][1] = w0.y, v[q][2] = w0.z, v[q][3] = w0.w;
+                v[q][4] = w1.x, v[q][5] = w1.y, v[q][6] = w1.z, v[q][7] = w1.w;
             }
         };
-        if (half < steps) load(half);
-        for (int j = half; j < steps; j += 2) {
+        if (first < steps) load(first);
+        for (int j = first; j < steps; j += stride) {
             const int s = j % S::kStages;
             bool ok = true;
             if (j >= S::kStages) ok = mbar_wait(&empty[s], ((j / S::kStages) - 1) & 1, deadline, &status);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
-            unsigned char* st = smem + (size_t)s * S::kStageBytes;
-            unsigned char* stw = st + S::kPartsX * kRgPlaneA;
+            unsigned char* st = smem + (size_t)s * S::kStageBytes + dst0;
 #pragma unroll
-            for (int q = 0; q < kQ; ++q) {
-                const int r = r0 + 32 * q;
-                uint4 o[3];
-                if constexpr (kBf16) {
-                    *reinterpret_cast<uint4*>(st + r * 128 + ((c8 ^ (r & 7)) << 4)) = xb[q];
-                } else {
-                    split8(xv[q], o);
-#pragma unroll
-                    for (int p = 0; p < 3; ++p)
-                        *reinterpret_cast<uint4*>(st + p * kRgPlaneA + r * 128 + ((c8 ^ (r & 7)) << 4)) = o[p];
-                }
-                if (r < g.ET) {
-                    const int eg = r >= g.EG ? 1 : 0;  // at most two expert groups
-                    split8(wv[q], o);
-#pragma unroll
-                    for (int p = 0; p < 3; ++p) {
-                        const int row = (eg * 3 + p) * g.EG + (r - eg * g.EG);
-                        *reinterpret_cast<uint4*>(stw + row * 128 + ((c8 ^ (row & 7)) << 4)) = o[p];
-                    }
-                }
-            }
+            for (int q = 0; q < kQ; ++q)
+                if (r0 + 32 * q < height) split8(v[q], st + q * 32 * 128, plane);
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&full[s]);
-            if (j + 2 < steps) load(j + 2);
+            if (j + stride < steps) load(j + stride);
         }
-    } else if (lane == 0) {
-        bool ok = true;
-        for (int j = 0; j < steps && ok; ++j) {
-            const int s = j % S::kStages;
-            ok = mbar_wait(&full[s], (j / S::kStages) & 1, deadline, &status);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t xs = smem_u32(smem + (size_t)s * S::kStageBytes), ws = xs + S::kPartsX * kRgPlaneA;
-#pragma unroll
-            for (int kk = 0; kk < kRgK / 16; ++kk) {
-                for (int eg = 0; eg < g.n_eg; ++eg) {
-                    const uint64_t bd = smem_desc_sw128(ws + (uint32_t)(eg * 3 * g.EG * 128) + kk * 32);
-#pragma unroll
-                    for (int p = 0; p < S::kPartsX; ++p)
-                        tc_mma_ss(tmem + (uint32_t)((eg * 3 + p) * g.EG), smem_desc_sw128(xs + p * kRgPlaneA + kk * 32), bd,
-                                  idesc_bf16((3 - p) * g.EG), p > 0 || (j | kk) != 0);
-                }
+    } else if (warp == kRgWarpTma) {
+        // ---------------- TMA: bf16 activations ----------------
+        if (kBf16 && lane == 0) {
+            int j = 0;
+            for (; j < steps; ++j) {
+                const int s = j % S::kStages;
+                if (j >= S::kStages && !mbar_wait(&empty[s], ((j / S::kStages) - 1) & 1, deadline, &status)) break;
+                mbar_expect_tx(&full[s], kRgPlaneA);
+                tma_load_2d(smem + (size_t)s * S::kStageBytes, &tx, k0 + j * kRgK, m0, &full[s]);
             }
-            tc_commit(&empty[s]);
+            // every issued copy lands before the CTA can retire (normally long done)
+            const unsigned long long drain = global_ns() + kRgDrainNs;
+            for (int i = max(0, j - S::kStages); i < j; ++i)
+                mbar_wait(&full[i % S::kStages], (i / S::kStages) & 1, drain, &status);
         }
-        tc_commit(&done);  // every MMA issued above completes before the accumulators are read
-    }
-    if (warp < kRgProducers / 32) {
-        const bool ok = mbar_wait(&done, 0, deadline, &status);
-        if (__all_sync(0xFFFFFFFFu, ok)) {
+    } else if (warp == kRgWarpMma) {
+        // ---------------- MMA issuer ----------------
+        if (lane == 0) {
+            const uint32_t n1 = idesc_bf16(ET), n2 = idesc_bf16(2 * ET);
+            for (int j = 0; j < steps; ++j) {
+                const int s = j % S::kStages, round = j / kRgRound, buf = round & 1;
+                if (j % kRgRound == 0 && round >= 2) {
+                    if (!mbar_wait(&acc_empty[buf], ((round >> 1) - 1) & 1, deadline, &status)) break;
+                    tc_fence_after();
+                }
+                if (!mbar_wait(&full[s], (j / S::kStages) & 1, deadline, &status)) break;
+                tc_fence_after();
+                const uint32_t xs = smem_u32(smem + (size_t)s * S::kStageBytes), ws = xs + S::kPartsX * kRgPlaneA;
+                const uint32_t o0 = tmem + buf * kRgMaxE, o12 = tmem + kRgO12;
+#pragma unroll
+                for (int kk = 0; kk < kRgK / 16; ++kk) {
+                    const uint64_t x0 = smem_desc_sw128(xs + kk * 32), w0 = smem_desc_sw128(ws + kk * 32);
+                    const uint64_t w1 = smem_desc_sw128(ws + ET * 128 + kk * 32);
+                    tc_mma_ss(o0, x0, w0, n1, j % kRgRound != 0 || kk != 0);
+                    tc_mma_ss(o12, x0, w1, n2, (j | kk) != 0);
+                    if constexpr (!kBf16) {
+                        tc_mma_ss(o12, smem_desc_sw128(xs + kRgPlaneA + kk * 32), w0, n2, 1);
+                        tc_mma_ss(o12 + ET, smem_desc_sw128(xs + 2 * kRgPlaneA + kk * 32), w0, n1, 1);
+                    }
+                }
+                tc_commit(&empty[s]);
+                if (j % kRgRound == kRgRound - 1 && j + 1 < steps) tc_commit(&acc_full[buf]);
+            }
+            tc_commit(&done);  // every MMA issued above completes before the last sums are read
+        }
+    } else {
+        // ---------------- epilogue (warps 16-19: TMEM lane quadrants 0-3) ----------------
+        const int qd = warp & 3, t = m0 + qd * 32 + lane;
+        const uint32_t lanes = (uint32_t)(qd * 32) << 16;
+        float* out = a.part + ((size_t)blockIdx.z * a.T + t) * a.Ep + e0;
+        for (int r = 0; r < rounds; ++r) {
+            const bool last = r == rounds - 1;
+            const bool ok = last ? mbar_wait(&done, 0, deadline, &status)
+                                 : mbar_wait(&acc_full[r & 1], (r >> 1) & 1, deadline, &status);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
             tc_fence_after();
-            const int qd = warp & 3, t = m0 + qd * 32 + lane;
-            float* out = a.part + ((size_t)blockIdx.z * a.T + t) * a.Ep + e0;
-            const int nb = g.ET / 16, per = g.EG / 16;
-            for (int b = warp >> 2; b < nb; b += 4) {
-                const int eg = b / per, c = (b - eg * per) * 16;
-                const uint32_t col = tmem + ((uint32_t)(qd * 32) << 16) + (uint32_t)(eg * 3 * g.EG + c);
-                float v0[16], v1[16], v2[16];
-                tmem_ld16(col, v0);
-                tmem_ld16(col + g.EG, v1);
-                tmem_ld16(col + 2 * g.EG, v2);
+            for (int c = 0; c < ET; c += 16) {
+                float v[16];
+                tmem_ld16(tmem + lanes + (r & 1) * kRgMaxE + c, v);
+                if (last) {
+                    float v1[16], v2[16];
+                    tmem_ld16(tmem + lanes + kRgO12 + c, v1);
+                    tmem_ld16(tmem + lanes + kRgO12 + ET + c, v2);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] += v1[i] + v2[i];
+                }
                 if (t < a.T) {
 #pragma unroll
                     for (int i = 0; i < 16; i += 4)
-                        if (e0 + 16 * b + i < a.Ep)
-                            *reinterpret_cast<float4*>(out + 16 * b + i) =
-                                make_float4(v0[i] + (v1[i] + v2[i]), v0[i + 1] + (v1[i + 1] + v2[i + 1]),
-                                            v0[i + 2] + (v1[i + 2] + v2[i + 2]), v0[i + 3] + (v1[i + 3] + v2[i + 3]));
+                        if (e0 + c + i < a.Ep) {
+                            if (r == 0) *reinterpret_cast<float4*>(out + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                            else red_add4(out + c + i, v[i], v[i + 1], v[i + 2], v[i + 3]);
+                        }
                 }
             }
+            tc_fence_before();
+            __syncwarp();
+            if (!last && lane == 0) mbar_arrive(&acc_empty[r & 1]);
         }
-        tc_fence_before();
     }
     __syncthreads();
     if (threadIdx.x == 0) a.cta_status[(blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x] = status;
-    if (warp == kRgProducers / 32) {
+    if (warp == kRgWarpMma) {
         if (lane == 0) mbar_wait(&done, 0, global_ns() + kRgDrainNs, &status);
         __syncwarp();
         tc_fence_after();
@@ -354,35 +372,70 @@ __device__ __forceinline__ float order_value(uint32_t m)
 }
 
 // Bound on the error of an fp32 choice score c = s + bias, from the bound dz on
-// z: sigmoid' <= 1/4; softmax moves by at most 2 s dz (its own z and the sum);
-// a few units in the last place of s and of the sum with the bias.
+// z: sigmoid' = s (1 - s), which itself moves by less than dz / 8; softmax moves by
+// at most 2 s dz (its own z and the sum); a few units in the last place of s and
+// of the sum with the bias.  A score that is not known exactly: s = 1/2 for the
+// sigmoid, the largest one for softmax.
 __device__ __forceinline__ float choice_err(int softmax, float s, float c, float dz)
 {
     if (!(fabsf(c) < 3.0e38f)) return 0.f;  // an infinite bias decides by itself
-    const float own = softmax ? s * (2.f * dz + 0x1p-20f) : 0.25f * dz + 0x1p-22f;
+    const float own = softmax ? s * (2.f * dz + 0x1p-20f) : (s * (1.f - s) + dz) * dz + 0x1p-22f;
     return own + 0x1p-23f * fabsf(c);
 }
 
-// z = x_t . w_e in double by one warp (the same order for every expert, so equal rows stay equal).
-__device__ __forceinline__ double route_dot(const RouteArgs& a, bool bf16, int t, int e)
+// z = x_t . w_e in double for up to four experts at once by one warp, read side by
+// side (the loads' latency is the cost).  The same order for every expert, so
+// equal rows stay equal.  Unused places repeat an expert.
+__device__ __forceinline__ void route_dot4(const RouteArgs& a, bool bf16, int t, const int (&e)[4], double (&z)[4])
 {
     const int lane = threadIdx.x & 31;
-    const float* wrow = a.w_router + (size_t)e * a.H;
     const char* xr = static_cast<const char*>(a.x) + (size_t)t * a.H * (bf16 ? 2 : 4);
-    double s0 = 0., s1 = 0., s2 = 0., s3 = 0.;
-#pragma unroll 8
-    for (int i = lane * 4; i < a.H; i += 128) {
-        const float4 w = *reinterpret_cast<const float4*>(wrow + i);
-        const float4 v = bf16 ? load_act4<true>(xr, i) : load_act4<false>(xr, i);
-        s0 = fma((double)w.x, (double)v.x, s0);
-        s1 = fma((double)w.y, (double)v.y, s1);
-        s2 = fma((double)w.z, (double)v.z, s2);
-        s3 = fma((double)w.w, (double)v.w, s3);
-    }
-    double s = (s0 + s1) + (s2 + s3);
+    const float* w[4];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    return s;
+    for (int j = 0; j < 4; ++j) {
+        w[j] = a.w_router + (size_t)e[j] * a.H;
+        z[j] = 0.;
+    }
+#pragma unroll 2
+    for (int i = lane * 4; i < a.H; i += 128) {
+        const float4 v = bf16 ? load_act4<true>(xr, i) : load_act4<false>(xr, i);
+        float4 u[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) u[j] = *reinterpret_cast<const float4*>(w[j] + i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            z[j] = fma((double)u[j].x, (double)v.x, z[j]);
+            z[j] = fma((double)u[j].y, (double)v.y, z[j]);
+            z[j] = fma((double)u[j].z, (double)v.z, z[j]);
+            z[j] = fma((double)u[j].w, (double)v.w, z[j]);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) z[j] += __shfl_xor_sync(0xFFFFFFFFu, z[j], o);
+    }
+}
+
+// Calls take(expert, z) in order for each bit of `bits` that names one (expert_of: bit -> expert).
+template <typename ExpertOf, typename Take>
+__device__ __forceinline__ void route_dots(const RouteArgs& a, bool bf16, int t, uint32_t bits, ExpertOf expert_of, Take take)
+{
+    while (bits) {
+        int e[4], b[4], n = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            b[j] = bits ? __ffs(bits) - 1 : b[0];
+            n += bits ? 1 : 0;
+            bits &= bits - 1;
+            e[j] = expert_of(b[j]);
+        }
+        double z[4];
+        route_dot4(a, bf16, t, e, z);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < n) take(b[j], e[j], z[j]);
+    }
 }
 
 __device__ __forceinline__ double warp_sum_d(double v)
@@ -582,18 +635,15 @@ __device__ __noinline__ void route_exact(const RouteArgs& a, bool bf16, int t, c
         }
         if (!marked) break;
         __syncwarp();
-        for (int b = 0; b < E; b += 32) {
-            uint32_t todo = __ballot_sync(full, b + lane < E && st[b + lane] == 2);
-            while (todo) {
-                const int e = b + __ffs(todo) - 1;
-                todo &= todo - 1;
-                const double v = route_dot(a, bf16, t, e);
-                if (lane == 0) {
-                    zd[e] = v;
-                    st[e] = 1;
-                }
-            }
-        }
+        for (int b = 0; b < E; b += 32)
+            route_dots(
+                a, bf16, t, __ballot_sync(full, b + lane < E && st[b + lane] == 2), [&](int i) { return b + i; },
+                [&](int, int e, double v) {
+                    if (lane == 0) {
+                        zd[e] = v;
+                        st[e] = 1;
+                    }
+                });
         __syncwarp();
     }
 }
@@ -639,14 +689,15 @@ __device__ __noinline__ bool route_close(const RouteArgs& a, bool bf16, int t, c
             const float floor_c = __shfl_sync(full, gs.last, g) - 2.f * gs.err;
             double v1 = -INFINITY, v2 = -INFINITY, p1 = 0., p2 = 0.;
             for (int b = g * m; b < (g + 1) * m; b += 32) {
-                uint32_t cand = __ballot_sync(full, b + lane < (g + 1) * m && c_s[at(b + lane)] >= floor_c);
-                for (; cand; cand &= cand - 1) {
-                    const int e = b + __ffs(cand) - 1;
-                    double p;
-                    const double v = choice_exact(a, e, route_dot(a, bf16, t, e), zm, den, p);
-                    if (v > v1) v2 = v1, p2 = p1, v1 = v, p1 = p;
-                    else if (v > v2) v2 = v, p2 = p;
-                }
+                const uint32_t cand = __ballot_sync(full, b + lane < (g + 1) * m && c_s[at(b + lane)] >= floor_c);
+                route_dots(
+                    a, bf16, t, cand, [&](int i) { return b + i; },
+                    [&](int, int e, double z) {
+                        double p;
+                        const double v = choice_exact(a, e, z, zm, den, p);
+                        if (v > v1) v2 = v1, p2 = p1, v1 = v, p1 = p;
+                        else if (v > v2) v2 = v, p2 = p;
+                    });
             }
             if (lane == g) sc = a.top == 2 ? v1 + v2 : v1, sp = a.top == 2 ? p1 + p2 : p1;
         }
@@ -696,14 +747,13 @@ __device__ __noinline__ bool route_close(const RouteArgs& a, bool bf16, int t, c
     const float nc = __shfl_down_sync(full, my_c, 1), nu = __shfl_down_sync(full, my_u, 1);
     const uint32_t open = __ballot_sync(full, lane + 1 < n && my_c - nc <= my_u + nu);
     double v = (double)my_c;
-    for (uint32_t left = open | (open << 1); left; left &= left - 1) {
-        const int j = __ffs(left) - 1;
-        const int e = __shfl_sync(full, my_e, j);
-        const double z = route_dot(a, bf16, t, e);
-        double p;
-        const double w = choice_exact(a, e, z, zm, den, p);
-        if (lane == j) v = w, my_p = p;
-    }
+    route_dots(
+        a, bf16, t, open | (open << 1), [&](int j) { return __shfl_sync(full, my_e, j); },
+        [&](int j, int e, double z) {
+            double p;
+            const double w = choice_exact(a, e, z, zm, den, p);
+            if (lane == j) v = w, my_p = p;
+        });
     // slot of each: runs stay in place, inside a run by the double sums (equal: lower expert first)
     const int run = __popc(~open & ((1u << lane) - 1u));
     int slot = 0;
@@ -742,7 +792,7 @@ __host__ __device__ __forceinline__ size_t route_token_smem(int E)
 // token selects.  kPer = experts per lane.  Latency-bound: k + 1 rounds of a
 // warp-wide maximum (one redux instruction) over order-preserving integer keys.
 template <int kPer, bool kBf16>
-__global__ void __launch_bounds__(kRouteThreads) route_select_kernel(const __grid_constant__ RouteArgs a, int tokens)
+__global__ void __launch_bounds__(kRouteThreads, kPer <= 8 ? 3 : 2) route_select_kernel(const __grid_constant__ RouteArgs a, int tokens)
 {
     extern __shared__ __align__(16) unsigned char route_smem[];
     const unsigned full = 0xFFFFFFFFu;
@@ -760,26 +810,27 @@ __global__ void __launch_bounds__(kRouteThreads) route_select_kernel(const __gri
         if (lane == 0) *a.status = bad;
     }
     {
-        const int Ep = a.Ep, Eq = Ep / 4;
-        const size_t plane = (size_t)a.T * Ep;
-        for (int i = threadIdx.x; i < nt * Eq; i += kRouteThreads) {
-            const int t = i / Eq, q = i - t * Eq;
-            const float* p = a.part + (size_t)(t0 + t) * Ep + 4 * q;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int s0 = 0; s0 < a.splits; s0 += 8) {  // eight independent loads at a time
-                float4 o[8];
+        const int Eq = a.Ep / 4;
+        const size_t plane = (size_t)a.T * a.Ep;
+        const int per = kRouteWarps / tokens;  // warps per token (tokens is a power of two)
+        const int wt = warp / per;
+        if (wt < nt) {
+            float* dst = reinterpret_cast<float*>(route_smem + wt * stride);
+            const float* row = a.part + (size_t)(t0 + wt) * a.Ep;
+            for (int q = (warp - wt * per) * 32 + lane; q < Eq; q += per * 32) {
+                const float* p = row + 4 * q;
+                float4 v = *reinterpret_cast<const float4*>(p);
+                for (int s0 = 1; s0 < a.splits; s0 += 8) {  // up to eight independent loads at a time
+                    float4 o[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    o[j] = s0 + j < a.splits ? *reinterpret_cast<const float4*>(p + (s0 + j) * plane)
-                                             : make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int j = 0; j < 8; ++j)
+                        if (s0 + j < a.splits) o[j] = *reinterpret_cast<const float4*>(p + (s0 + j) * plane);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v.x += o[j].x, v.y += o[j].y, v.z += o[j].z, v.w += o[j].w;
+                    for (int j = 0; j < 8; ++j)
+                        if (s0 + j < a.splits) v.x += o[j].x, v.y += o[j].y, v.z += o[j].z, v.w += o[j].w;
+                }
+                *reinterpret_cast<float4*>(dst + 4 * q) = v;  // the row's padding has room
             }
-            float* dst = reinterpret_cast<float*>(route_smem + t * stride) + 4 * q;
-            const float r[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (4 * q + j < E) dst[j] = r[j];
         }
     }
     __syncthreads();
@@ -853,7 +904,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_select_kernel(const __gri
             b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
             b1 = fmaxf(b1, o1);
         }
-        const float s_most = 1.f / den;  // no softmax score is larger
+        const float s_most = a.softmax ? 1.f / den : 0.5f;
         float err = choice_err(a.softmax, s_most, b1, dz);
         float score = b1;
         if (a.top == 2) {
