@@ -335,6 +335,48 @@ COLI_API coli_status coli_router_forward(const coli_router* router, const void* 
                                          int32_t* topk_idx, float* topk_w, void* workspace, size_t ws_bytes,
                                          cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The residual path around a block (the pages name the decoder's layers, not its
+ * norms: root-mean-square norms before and after a block, with a gate and scales on
+ * the way back into the residual, are this library's reading of a decoder block).
+ */
+typedef enum {
+    COLI_GATE_NONE = 0,
+    COLI_GATE_CHANNEL = 1, /* gate [H] */
+    COLI_GATE_TOKEN = 2,   /* gate [T] */
+    COLI_GATE_ELEMENT = 3  /* gate [T, H] */
+} coli_gate;
+
+typedef struct coli_block_norm {
+    int hidden;           /* H, 1 .. 16384 (multiples of 8 are read in 16-byte vectors) */
+    float eps;            /* added to both means */
+    const float* post_w;  /* [H] weights of the norm of the block's output, or NULL: no such norm */
+    const float* pre_w;   /* [H] weights of the norm of the new residual (the next block's input), or NULL */
+    coli_gate gate;       /* what the block's output is multiplied with */
+    int gate_sigmoid;     /* 1: with sigmoid(gate) */
+    float residual_scale; /* factor of the old residual */
+    float block_scale;    /* factor of the (normalised, gated) block output */
+} coli_block_norm;
+
+/*
+ * One step of the residual path, per token t and channel h:
+ *   d  = block_out[t, h];  with post_w: d *= post_w[h] / sqrt(mean_h(block_out[t]^2) + eps)
+ *   d *= gate (or sigmoid(gate)) of the channel, the token or the element
+ *   r' = residual_scale * residual[t, h] + block_scale * d        -> residual_out[t, h]
+ *   y  = r' * pre_w[h] / sqrt(mean_h(r'[t]^2) + eps)              -> normed_out[t, h]
+ * Computed in fp32; y is taken from r' before its rounding to rt; every output is
+ * rounded once (to nearest even).  block_out, gate and normed_out have dtype xt,
+ * residual and residual_out dtype rt (an fp32 residual beside bf16 activations is
+ * allowed); all [T, H] row-major, 16-byte aligned.
+ * block_out NULL: no block ran (d = 0; neither post_w nor a gate).  residual_out
+ * NULL: not written.  normed_out is given exactly when norm->pre_w is.  An output
+ * may be the same tensor as an input of its dtype and shape (in place); any other
+ * overlap is refused.  T == 0 launches nothing.
+ */
+COLI_API coli_status coli_residual_norm(const coli_block_norm* norm, const void* block_out, coli_dtype xt,
+                                        const void* residual, coli_dtype rt, const void* gate, int T,
+                                        void* residual_out, void* normed_out, cudaStream_t stream);
+
 COLI_API const char* coli_status_string(coli_status status);
 COLI_API const char* coli_last_error(void);
 

@@ -52,6 +52,8 @@ _lib.coli_router_workspace_size.restype = ctypes.c_size_t
 _lib.coli_router_workspace_size.argtypes = [_p, _i]
 _lib.coli_router_forward.restype = _i
 _lib.coli_router_forward.argtypes = [_p, _p, _i, _i, _p, _p, _p, ctypes.c_size_t, _p]
+_lib.coli_residual_norm.restype = _i
+_lib.coli_residual_norm.argtypes = [_p, _p, _i, _p, _i, _p, _i, _p, _p, _p]
 _lib.coli_debug_set_wait_ns.restype = None
 _lib.coli_debug_set_wait_ns.argtypes = [ctypes.c_ulonglong]
 _lib.coli_debug_phase_stamps.restype = None
@@ -77,6 +79,11 @@ class _RouterStruct(ctypes.Structure):
     _fields_ = [("hidden", _i), ("n_experts", _i), ("top_k", _i), ("score", _i), ("n_group", _i),
                 ("topk_group", _i), ("group_top", _i), ("renormalise", _i), ("routed_scale", ctypes.c_float),
                 ("w_router", _p), ("sel_bias", _p)]
+
+
+class _BlockNormStruct(ctypes.Structure):
+    _fields_ = [("hidden", _i), ("eps", ctypes.c_float), ("post_w", _p), ("pre_w", _p), ("gate", _i),
+                ("gate_sigmoid", _i), ("residual_scale", ctypes.c_float), ("block_scale", ctypes.c_float)]
 
 
 def lib():
@@ -209,6 +216,51 @@ def router_forward(router, x, topk_idx, topk_w, workspace, stream=None):
     _check_tensor(topk_w, "topk_w", (T, router.top_k), (torch.float32,))
     _check(_lib.coli_router_forward(router.ref, x.data_ptr(), _dtype_code(x), T, topk_idx.data_ptr(), topk_w.data_ptr(),
                                     workspace.data_ptr(), workspace.nbytes, _stream_of(x, stream)))
+
+
+GATES = {"none": 0, "channel": 1, "token": 2, "element": 3}
+
+
+class BlockNorm:
+    """The residual path around a block of width H: norm weights [H] fp32 of the
+    block's output (post_w) and of the new residual (pre_w), each optional, the
+    gate's layout and the scales; see coli_block_norm in include/coli.h."""
+
+    def __init__(self, hidden, post_w=None, pre_w=None, eps=1e-5, gate="none", gate_sigmoid=False, residual_scale=1.0,
+                 block_scale=1.0):
+        import torch
+        for name, w in (("post_w", post_w), ("pre_w", pre_w)):
+            if w is not None:
+                _check_tensor(w, name, (hidden,), (torch.float32,))
+        self.tensors = dict(post_w=post_w, pre_w=pre_w)
+        self.hidden, self.gate = hidden, gate
+        self.struct = _BlockNormStruct(hidden, float(eps), _ptr(post_w), _ptr(pre_w), GATES[gate],
+                                       1 if gate_sigmoid else 0, float(residual_scale), float(block_scale))
+        self.ref = ctypes.byref(self.struct)
+
+
+def residual_norm(norm, residual, block_out, residual_out, normed_out, gate=None, stream=None):
+    """residual_out = residual_scale * residual + block_scale * gate * norm(block_out)
+    and normed_out = norm(residual_out), each [T, H].  block_out, residual_out and
+    normed_out may be None (see coli_residual_norm in include/coli.h)."""
+    import torch
+    T, H = residual.shape
+    real = (torch.bfloat16, torch.float32)
+    _check_tensor(residual, "residual", (T, norm.hidden), real)
+    xt = block_out if block_out is not None else normed_out if normed_out is not None else residual
+    if block_out is not None:
+        _check_tensor(block_out, "block_out", (T, H), real)
+    if residual_out is not None:
+        _check_tensor(residual_out, "residual_out", (T, H), (residual.dtype,))
+    if normed_out is not None:
+        _check_tensor(normed_out, "normed_out", (T, H), (xt.dtype,))
+    if gate is not None:
+        shape = {"channel": (H,), "token": (T,), "element": (T, H)}.get(norm.gate)
+        if shape is None:
+            raise ValueError("the norm has no gate")
+        _check_tensor(gate, "gate", shape, (xt.dtype,))
+    _check(_lib.coli_residual_norm(norm.ref, _ptr(block_out), _dtype_code(xt), residual.data_ptr(), _dtype_code(residual),
+                                   _ptr(gate), T, _ptr(residual_out), _ptr(normed_out), _stream_of(residual, stream)))
 
 
 def expert_union(topk_idx, E, count, offset, active, n_active, perm, inv_perm, stream=None):
