@@ -377,6 +377,44 @@ COLI_API coli_status coli_residual_norm(const coli_block_norm* norm, const void*
                                         const void* residual, coli_dtype rt, const void* gate, int T,
                                         void* residual_out, void* normed_out, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Low-rank adapters of many requests at once, beside a projection that they share
+ * (the pages describe one model for one user; adapters are an addition of this
+ * library for serving several).
+ */
+typedef struct coli_adapters {
+    int in_features;     /* K: a multiple of 8, at most 65536 */
+    int out_features;    /* N: a multiple of 8, at most 65536 */
+    int max_rank;        /* R: a multiple of 8, at most 256 */
+    int n_adapters;      /* n: 1 .. 1024 */
+    const uint16_t* a;   /* [n, R, K] bf16 */
+    const uint16_t* b;   /* [n, N, R] bf16 */
+    const float* scale;  /* [n] fp32 (device) */
+    const int32_t* rank; /* [n] rank of each adapter, 0 .. R (device), or NULL: all R.  Rows of a and columns of b
+                            behind it are not used, whatever they hold */
+} coli_adapters;
+
+/* Bytes of workspace coli_adapters_forward needs for T tokens (0 if the
+ * description or T is invalid).  Decided by the shapes alone. */
+COLI_API size_t coli_adapters_workspace_size(const coli_adapters* adapters, int T);
+
+/*
+ * out[t] = base[t] + scale[i] * b[i] (a[i] x[t]) with i = which[t], for x [T, K]
+ * (dtype xt), base and out [T, N] (dtype ot), which int32 [T] (device).  A token
+ * whose which is outside [0, n) has no adapter: out[t] = base[t].  The tokens may
+ * come in any order.  base NULL stands for zeros; base may be out (in place: the
+ * rows of tokens without an adapter are not touched); any other overlap of out
+ * with base or x is refused.  Products are exact and summed in fp32; with bf16
+ * outputs the inner result enters the second product with 16 bits (2^-16
+ * relative); out is rounded once.  A non-finite activation makes its own row of
+ * out non-finite (NaN where a sum would be infinite).  Deterministic.  Workspace as in
+ * coli_router_forward (256-byte aligned, undefined on entry, not shared by calls
+ * that may run concurrently).  T == 0 launches nothing.
+ */
+COLI_API coli_status coli_adapters_forward(const coli_adapters* adapters, const void* x, coli_dtype xt, int T,
+                                           const int32_t* which, const void* base, void* out, coli_dtype ot,
+                                           void* workspace, size_t ws_bytes, cudaStream_t stream);
+
 COLI_API const char* coli_status_string(coli_status status);
 COLI_API const char* coli_last_error(void);
 

@@ -54,6 +54,10 @@ _lib.coli_router_forward.restype = _i
 _lib.coli_router_forward.argtypes = [_p, _p, _i, _i, _p, _p, _p, ctypes.c_size_t, _p]
 _lib.coli_residual_norm.restype = _i
 _lib.coli_residual_norm.argtypes = [_p, _p, _i, _p, _i, _p, _i, _p, _p, _p]
+_lib.coli_adapters_workspace_size.restype = ctypes.c_size_t
+_lib.coli_adapters_workspace_size.argtypes = [_p, _i]
+_lib.coli_adapters_forward.restype = _i
+_lib.coli_adapters_forward.argtypes = [_p, _p, _i, _i, _p, _p, _p, _i, _p, ctypes.c_size_t, _p]
 _lib.coli_debug_set_wait_ns.restype = None
 _lib.coli_debug_set_wait_ns.argtypes = [ctypes.c_ulonglong]
 _lib.coli_debug_phase_stamps.restype = None
@@ -84,6 +88,11 @@ class _RouterStruct(ctypes.Structure):
 class _BlockNormStruct(ctypes.Structure):
     _fields_ = [("hidden", _i), ("eps", ctypes.c_float), ("post_w", _p), ("pre_w", _p), ("gate", _i),
                 ("gate_sigmoid", _i), ("residual_scale", ctypes.c_float), ("block_scale", ctypes.c_float)]
+
+
+class _AdaptersStruct(ctypes.Structure):
+    _fields_ = [("in_features", _i), ("out_features", _i), ("max_rank", _i), ("n_adapters", _i), ("a", _p), ("b", _p),
+                ("scale", _p), ("rank", _p)]
 
 
 def lib():
@@ -261,6 +270,50 @@ def residual_norm(norm, residual, block_out, residual_out, normed_out, gate=None
         _check_tensor(gate, "gate", shape, (xt.dtype,))
     _check(_lib.coli_residual_norm(norm.ref, _ptr(block_out), _dtype_code(xt), residual.data_ptr(), _dtype_code(residual),
                                    _ptr(gate), T, _ptr(residual_out), _ptr(normed_out), _stream_of(residual, stream)))
+
+
+class Adapters:
+    """Low-rank adapters stacked for one projection: a [n, R, K] and b [n, N, R]
+    bf16, scale [n] fp32, rank [n] int32 (None: all R); see coli_adapters in
+    include/coli.h."""
+
+    def __init__(self, a, b, scale, rank=None):
+        import torch
+        n, R, K = a.shape
+        N = b.shape[1]
+        _check_tensor(a, "a", (n, R, K), (torch.bfloat16,))
+        _check_tensor(b, "b", (n, N, R), (torch.bfloat16,))
+        _check_tensor(scale, "scale", (n,), (torch.float32,))
+        if rank is not None:
+            _check_tensor(rank, "rank", (n,), (torch.int32,))
+        self.tensors = dict(a=a, b=b, scale=scale, rank=rank)
+        self.in_features, self.out_features = K, N
+        self.struct = _AdaptersStruct(K, N, R, n, _ptr(a), _ptr(b), _ptr(scale), _ptr(rank))
+        self.ref = ctypes.byref(self.struct)
+
+
+def adapters_workspace_size(adapters, T):
+    """Bytes of workspace adapters_forward needs for T tokens."""
+    n = int(_lib.coli_adapters_workspace_size(adapters.ref, T))
+    if n == 0:
+        raise ColiError(1)
+    return n
+
+
+def adapters_forward(adapters, x, which, out, workspace, base=None, stream=None):
+    """out [T, N] = base [T, N] + the adapter which[t] of each row of x [T, K];
+    which is int32 [T], outside [0, n) for no adapter.  base may be out or None."""
+    import torch
+    T = x.shape[0]
+    real = (torch.bfloat16, torch.float32)
+    _check_tensor(x, "x", (T, adapters.in_features), real)
+    _check_tensor(which, "which", (T,), (torch.int32,))
+    _check_tensor(out, "out", (T, adapters.out_features), real)
+    if base is not None:
+        _check_tensor(base, "base", (T, adapters.out_features), (out.dtype,))
+    _check(_lib.coli_adapters_forward(adapters.ref, x.data_ptr(), _dtype_code(x), T, which.data_ptr(), _ptr(base),
+                                      out.data_ptr(), _dtype_code(out), workspace.data_ptr(), workspace.nbytes,
+                                      _stream_of(x, stream)))
 
 
 def expert_union(topk_idx, E, count, offset, active, n_active, perm, inv_perm, stream=None):

@@ -1,0 +1,123 @@
+// coli_adapters.cu -- host side of the low-rank adapters (coli_adapters_forward).
+#include <algorithm>
+
+#include "coli_adapters.cuh"
+#include "coli_host.h"
+
+using namespace coli;
+
+namespace {
+
+constexpr int kSms = 148;  // grid sizing (B200)
+
+coli_status check_adapters(const coli_adapters* d, int T)
+{
+    if (!d) return fail(COLI_ERR_INVALID_ARG, "adapters is NULL");
+    if (T < 0 || T > kMaxTokens) return fail(COLI_ERR_INVALID_ARG, "T=%d outside [0, %d]", T, kMaxTokens);
+    if (d->in_features < 8 || d->in_features % 8 != 0 || d->in_features > 65536)
+        return fail(COLI_ERR_INVALID_ARG, "in_features=%d is not a multiple of 8 in [8, 65536]", d->in_features);
+    if (d->out_features < 8 || d->out_features % 8 != 0 || d->out_features > 65536)
+        return fail(COLI_ERR_INVALID_ARG, "out_features=%d is not a multiple of 8 in [8, 65536]", d->out_features);
+    if (d->max_rank < 8 || d->max_rank % 8 != 0 || d->max_rank > kLoMaxRank)
+        return fail(COLI_ERR_INVALID_ARG, "max_rank=%d is not a multiple of 8 in [8, %d]", d->max_rank, kLoMaxRank);
+    if (d->n_adapters < 1 || d->n_adapters > kMaxExperts)
+        return fail(COLI_ERR_INVALID_ARG, "n_adapters=%d outside [1, %d]", d->n_adapters, kMaxExperts);
+    if (!d->a || !d->b || !d->scale) return fail(COLI_ERR_INVALID_ARG, "adapters.a / b / scale is NULL");
+    if (!aligned(d->a, 16) || !aligned(d->b, 16)) return fail(COLI_ERR_INVALID_ARG, "adapters.a / b not 16-byte aligned");
+    if (!aligned(d->scale, 4) || !aligned(d->rank, 4))
+        return fail(COLI_ERR_INVALID_ARG, "adapters.scale / rank not 4-byte aligned");
+    return COLI_OK;
+}
+
+struct LoPlan {
+    int max_tiles, pieces, chunk, cols;
+    size_t perm, tiles, n_tiles, bytes;  // workspace offsets (partial sums of h first)
+};
+
+LoPlan lo_plan(const coli_adapters* d, int T)
+{
+    LoPlan p{};
+    // tiles of T tokens over g groups: at most T / 32 whole ones and one more per group
+    p.max_tiles = std::max(1, T / kLoTile + std::min(T, d->n_adapters + 1));
+    // pieces of K that give about two blocks per SM, each with at least one 32-K block for every warp
+    const int most = std::max(1, d->in_features / (32 * kLoWarps));
+    p.pieces = std::max(1, std::min(most, 2 * kSms / p.max_tiles));
+    p.chunk = ((d->in_features + p.pieces - 1) / p.pieces + 32 * kLoWarps - 1) / (32 * kLoWarps) * (32 * kLoWarps);
+    p.pieces = (d->in_features + p.chunk - 1) / p.chunk;
+    // columns per block: as many as leave about four blocks per SM, whole rounds of the warps' 32
+    const int units = (d->out_features + 32 * kLoWarps - 1) / (32 * kLoWarps);
+    const int want = std::max(1, std::min(units, 4 * kSms / p.max_tiles));
+    p.cols = (units + want - 1) / want * 32 * kLoWarps;
+    size_t off = align_up((size_t)p.pieces * T * d->max_rank * 4, 256);
+    const bool big = T > kLoSmallT;
+    p.perm = off;
+    off += align_up(big ? (size_t)T * 4 : 0, 256);
+    p.tiles = off;
+    off += align_up(big ? (size_t)p.max_tiles * 12 : 0, 256);
+    p.n_tiles = off;
+    p.bytes = off + 256;
+    return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t coli_adapters_workspace_size(const coli_adapters* d, int T)
+{
+    if (check_adapters(d, T) != COLI_OK) return 0;
+    return lo_plan(d, T).bytes;
+}
+
+coli_status coli_adapters_forward(const coli_adapters* d, const void* x, coli_dtype xt, int T, const int32_t* which,
+                                  const void* base, void* out, coli_dtype ot, void* workspace, size_t ws_bytes,
+                                  cudaStream_t stream)
+{
+    coli_status st = check_adapters(d, T);
+    if (st != COLI_OK) return st;
+    if (!known_dtype(xt)) return fail(COLI_ERR_INVALID_ARG, "unknown activation dtype %d", (int)xt);
+    if (!known_dtype(ot)) return fail(COLI_ERR_INVALID_ARG, "unknown output dtype %d", (int)ot);
+    if (T == 0) return COLI_OK;
+    if (!x || !which || !out || !workspace) return fail(COLI_ERR_INVALID_ARG, "NULL pointer argument");
+    if (!aligned(x, 16) || !aligned(base, 16) || !aligned(out, 16))
+        return fail(COLI_ERR_INVALID_ARG, "x / base / out not 16-byte aligned");
+    if (!aligned(which, 4)) return fail(COLI_ERR_INVALID_ARG, "which not 4-byte aligned");
+    if (!aligned(workspace, 256)) return fail(COLI_ERR_INVALID_ARG, "workspace not 256-byte aligned");
+    const size_t nx = (size_t)T * d->in_features * dtype_size(xt), no = (size_t)T * d->out_features * dtype_size(ot);
+    if (overlap(x, nx, out, no)) return fail(COLI_ERR_INVALID_ARG, "out overlaps x");
+    if (base != out && overlap(base, no, out, no)) return fail(COLI_ERR_INVALID_ARG, "out overlaps base without being the same tensor");
+    const LoPlan p = lo_plan(d, T);
+    if (ws_bytes < p.bytes) return fail(COLI_ERR_WORKSPACE, "workspace %zu bytes, need %zu", ws_bytes, p.bytes);
+
+    char* ws = static_cast<char*>(workspace);
+    LoArgs a{};
+    a.T = T, a.K = d->in_features, a.N = d->out_features, a.R = d->max_rank, a.n = d->n_adapters;
+    a.x = x, a.a = d->a, a.b = d->b, a.rank = d->rank, a.scale = d->scale, a.which = which, a.base = base, a.out = out;
+    a.h = reinterpret_cast<float*>(ws);
+    a.pieces = p.pieces, a.chunk = p.chunk, a.cols = p.cols, a.max_tiles = p.max_tiles;
+    a.perm = reinterpret_cast<int32_t*>(ws + p.perm);
+    a.tiles = reinterpret_cast<int32_t*>(ws + p.tiles);
+    a.n_tiles = reinterpret_cast<int32_t*>(ws + p.n_tiles);
+
+    cudaError_t e = cudaSuccess;
+    const dim3 g1(p.max_tiles, p.pieces), g2(p.max_tiles, (a.N + a.cols - 1) / a.cols);
+    if (T > kLoSmallT) {
+        lo_group_kernel<<<1, kLoGroupThreads, 0, stream>>>(a);
+        if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "adapter grouping launch");
+        e = launch_pdl(xt == COLI_BF16 ? lo_shrink_kernel<true> : lo_shrink_kernel<false>, g1, kLoThreads, 0, stream, a);
+    } else {
+        if (xt == COLI_BF16) lo_shrink_kernel<true><<<g1, kLoThreads, 0, stream>>>(a);
+        else lo_shrink_kernel<false><<<g1, kLoThreads, 0, stream>>>(a);
+        e = cudaGetLastError();
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "adapter shrink launch");
+    const size_t rs = (size_t)(a.R + 31) / 32 * 32 + 8;
+    const size_t smem = (ot == COLI_BF16 ? 2 : 3) * kLoTile * rs * 2;
+    auto kern = ot == COLI_BF16 ? lo_expand_kernel<true> : lo_expand_kernel<false>;
+    if (smem > 46 * 1024 && (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
+        return cuda_fail(e, "kernel attribute setup");
+    e = launch_pdl(kern, g2, kLoThreads, smem, stream, a);
+    return e == cudaSuccess ? COLI_OK : cuda_fail(e, "adapter expand launch");
+}
+
+}  // extern "C"
