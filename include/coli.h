@@ -69,7 +69,7 @@ typedef struct coli_moe_layer {
     int top_k;             /* k, e.g. 8 */
     int group;             /* scale group along K; must be 64 */
     float routed_scale;    /* factor applied to the renormalised routed weights, e.g. 2.5 */
-    const float* w_router; /* [E, H] fp32 */
+    const float* w_router; /* [E, H] fp32; with sel_bias NULL for a layer whose routing is always given */
     const float* sel_bias; /* [E] fp32, selection-only bias */
     const uint8_t* gate_q; /* [E+1, F, H/2] */
     const uint8_t* up_q;   /* [E+1, F, H/2] */
@@ -185,6 +185,21 @@ COLI_API size_t coli_moe_status_word_offset(const coli_moe_layer* layer, int T);
 COLI_API coli_status coli_moe_forward(const coli_moe_layer* layer, const void* x, coli_dtype xt, int T,
                              void* out, coli_dtype ot, void* workspace, size_t ws_bytes,
                              int32_t* topk_idx_out, float* topk_w_out, cudaStream_t stream);
+
+/*
+ * The layer with the routing given (from coli_router_forward, or any other source):
+ * coli_moe_forward without its Route step.  topk_idx int32 [T, k] and topk_w fp32
+ * [T, k] are read on the device; k is layer->top_k.
+ *   out_t = sum_j topk_w[t, j] * FFN_{topk_idx[t, j]}(x_t) + FFN_shared(x_t)
+ * An index outside [0, E) is a dropped slot that costs nothing; an expert named
+ * twice by a token counts with the sum of its weights.  The layer's routed_scale,
+ * top_p and selection bias do not apply, and its w_router and sel_bias may both be
+ * NULL.  Everything else (paths, workspace, status word, act_int8) is as in
+ * coli_moe_forward.
+ */
+COLI_API coli_status coli_moe_forward_routed(const coli_moe_layer* layer, const void* x, coli_dtype xt, int T,
+                                             const int32_t* topk_idx, const float* topk_w, void* out, coli_dtype ot,
+                                             void* workspace, size_t ws_bytes, cudaStream_t stream);
 
 /* Kernel chains of coli_moe_forward (coli_moe_path). */
 enum {
@@ -414,6 +429,42 @@ COLI_API size_t coli_adapters_workspace_size(const coli_adapters* adapters, int 
 COLI_API coli_status coli_adapters_forward(const coli_adapters* adapters, const void* x, coli_dtype xt, int T,
                                            const int32_t* which, const void* base, void* out, coli_dtype ot,
                                            void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * One decoder block around the layer: the calls above in the order a decoder makes
+ * them.  All members are described where their types are.
+ */
+typedef struct coli_moe_block {
+    const coli_moe_layer* layer;
+    const coli_router* router;          /* of the layer's hidden, n_experts and top_k; NULL: the layer's own router */
+    const coli_block_norm* norm_before; /* the previous block's output into the residual, and the layer's input (pre_w set) */
+    const coli_block_norm* norm_after;  /* the layer's output into the residual, and the next block's input (if pre_w is set) */
+    const coli_adapters* adapters;      /* [H -> H] adapters added to the layer's output, or NULL */
+} coli_moe_block;
+
+/* Bytes of workspace coli_moe_block_forward needs (0 if the block, xt or T is invalid). */
+COLI_API size_t coli_moe_block_workspace_size(const coli_moe_block* block, coli_dtype xt, int T);
+
+/* Byte offsets in that workspace of the router's and the layer's status words
+ * (coli_router_forward, coli_moe_status_word_offset); SIZE_MAX where a call does
+ * not write one. */
+COLI_API coli_status coli_moe_block_status_word_offsets(const coli_moe_block* block, coli_dtype xt, int T, size_t* router,
+                                                        size_t* layer);
+
+/*
+ *   residual_out, x = coli_residual_norm(norm_before, prev_out, residual, gate_before)
+ *   y               = the layer on x (routed by block->router, or by itself), plus its adapters
+ *   residual_out, next_in = coli_residual_norm(norm_after, y, residual_out, gate_after)
+ * prev_out [T, H] xt is the previous block's output (NULL as in coli_residual_norm),
+ * residual and residual_out [T, H] rt (may be the same tensor), next_in [T, H] xt
+ * (given exactly when norm_after has pre_w), which int32 [T] with adapters.  x and
+ * y stay in the workspace in dtype xt.  Every step is checked before the first is
+ * enqueued.  T == 0 launches nothing.
+ */
+COLI_API coli_status coli_moe_block_forward(const coli_moe_block* block, const void* prev_out, coli_dtype xt,
+                                            const void* residual, coli_dtype rt, const void* gate_before,
+                                            const void* gate_after, const int32_t* which, int T, void* residual_out,
+                                            void* next_in, void* workspace, size_t ws_bytes, cudaStream_t stream);
 
 COLI_API const char* coli_status_string(coli_status status);
 COLI_API const char* coli_last_error(void);

@@ -58,6 +58,14 @@ _lib.coli_adapters_workspace_size.restype = ctypes.c_size_t
 _lib.coli_adapters_workspace_size.argtypes = [_p, _i]
 _lib.coli_adapters_forward.restype = _i
 _lib.coli_adapters_forward.argtypes = [_p, _p, _i, _i, _p, _p, _p, _i, _p, ctypes.c_size_t, _p]
+_lib.coli_moe_forward_routed.restype = _i
+_lib.coli_moe_forward_routed.argtypes = [_p, _p, _i, _i, _p, _p, _p, _i, _p, ctypes.c_size_t, _p]
+_lib.coli_moe_block_workspace_size.restype = ctypes.c_size_t
+_lib.coli_moe_block_workspace_size.argtypes = [_p, _i, _i]
+_lib.coli_moe_block_status_word_offsets.restype = _i
+_lib.coli_moe_block_status_word_offsets.argtypes = [_p, _i, _i, _p, _p]
+_lib.coli_moe_block_forward.restype = _i
+_lib.coli_moe_block_forward.argtypes = [_p, _p, _i, _p, _i, _p, _p, _p, _i, _p, _p, _p, ctypes.c_size_t, _p]
 _lib.coli_debug_set_wait_ns.restype = None
 _lib.coli_debug_set_wait_ns.argtypes = [ctypes.c_ulonglong]
 _lib.coli_debug_phase_stamps.restype = None
@@ -93,6 +101,10 @@ class _BlockNormStruct(ctypes.Structure):
 class _AdaptersStruct(ctypes.Structure):
     _fields_ = [("in_features", _i), ("out_features", _i), ("max_rank", _i), ("n_adapters", _i), ("a", _p), ("b", _p),
                 ("scale", _p), ("rank", _p)]
+
+
+class _BlockStruct(ctypes.Structure):
+    _fields_ = [("layer", _p), ("router", _p), ("norm_before", _p), ("norm_after", _p), ("adapters", _p)]
 
 
 def lib():
@@ -347,6 +359,83 @@ def moe_forward(layer, x, out, workspace, topk_idx_out=None, topk_w_out=None, st
     _check(_lib.coli_moe_forward(layer.ref, _ptr(x), _dtype_code(x), T, _ptr(out), _dtype_code(out),
                                  _ptr(workspace), workspace.numel() * workspace.element_size(),
                                  _ptr(topk_idx_out), _ptr(topk_w_out), _stream(stream)))
+
+
+def moe_forward_routed(layer, x, topk_idx, topk_w, out, workspace, stream=None):
+    """moe_forward with the routing given: topk_idx [T, k] int32 and topk_w [T, k]
+    fp32, e.g. from router_forward; see include/coli.h."""
+    import torch
+    T = x.shape[0]
+    real = (torch.bfloat16, torch.float32)
+    _check_tensor(x, "x", (T, layer.hidden), real)
+    _check_tensor(topk_idx, "topk_idx", (T, layer.top_k), (torch.int32,))
+    _check_tensor(topk_w, "topk_w", (T, layer.top_k), (torch.float32,))
+    _check_tensor(out, "out", (T, layer.hidden), real)
+    _check(_lib.coli_moe_forward_routed(layer.ref, x.data_ptr(), _dtype_code(x), T, topk_idx.data_ptr(), topk_w.data_ptr(),
+                                        out.data_ptr(), _dtype_code(out), workspace.data_ptr(), workspace.nbytes,
+                                        _stream_of(x, stream)))
+
+
+class Block:
+    """A decoder block around a layer: norms before and after, optionally a router
+    of its own and adapters beside the layer; see coli_moe_block in include/coli.h."""
+
+    def __init__(self, layer, norm_before, norm_after, router=None, adapters=None):
+        self.layer, self.norm_before, self.norm_after = layer, norm_before, norm_after
+        self.router, self.adapters = router, adapters
+        self.struct = _BlockStruct(*[None if m is None else ctypes.addressof(m.struct)
+                                     for m in (layer, router, norm_before, norm_after, adapters)])
+        self.ref = ctypes.byref(self.struct)
+
+
+def _dtype_of(dtype):
+    import torch
+    return {torch.float32: F32, torch.bfloat16: BF16}[dtype]
+
+
+def moe_block_workspace_size(block, dtype, T):
+    """Bytes of workspace moe_block_forward needs for T tokens of activations of a torch dtype."""
+    n = int(_lib.coli_moe_block_workspace_size(block.ref, _dtype_of(dtype), T))
+    if n == 0:
+        raise ColiError(1)
+    return n
+
+
+def moe_block_status_word_offsets(block, dtype, T):
+    """(router's, layer's) byte offsets of the status words in the workspace, None where there is none."""
+    r, l = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(_lib.coli_moe_block_status_word_offsets(block.ref, _dtype_of(dtype), T, ctypes.byref(r), ctypes.byref(l)))
+    return tuple(None if v.value == ctypes.c_size_t(-1).value else v.value for v in (r, l))
+
+
+def moe_block_forward(block, residual, prev_out, residual_out, next_in, workspace, which=None, gate_before=None,
+                      gate_after=None, stream=None):
+    """One block: prev_out into the residual, the layer (and its adapters) on the
+    normalised residual, its output into the residual, and next_in, the next
+    block's input (None when norm_after has no pre_w).  The activations' dtype is
+    prev_out's, or next_in's where prev_out is None; see include/coli.h."""
+    import torch
+    T, H = residual.shape
+    real = (torch.bfloat16, torch.float32)
+    _check_tensor(residual, "residual", (T, block.layer.hidden), real)
+    _check_tensor(residual_out, "residual_out", (T, H), (residual.dtype,))
+    act = prev_out if prev_out is not None else next_in if next_in is not None else residual
+    if prev_out is not None:
+        _check_tensor(prev_out, "prev_out", (T, H), real)
+    if next_in is not None:
+        _check_tensor(next_in, "next_in", (T, H), (act.dtype,))
+    for name, gate, norm in (("gate_before", gate_before, block.norm_before), ("gate_after", gate_after, block.norm_after)):
+        if gate is not None:
+            shape = {"channel": (H,), "token": (T,), "element": (T, H)}.get(norm.gate)
+            if shape is None:
+                raise ValueError(f"{name}: the norm has no gate")
+            _check_tensor(gate, name, shape, (act.dtype,))
+    if which is not None:
+        _check_tensor(which, "which", (T,), (torch.int32,))
+    _check(_lib.coli_moe_block_forward(block.ref, _ptr(prev_out), _dtype_code(act), residual.data_ptr(),
+                                       _dtype_code(residual), _ptr(gate_before), _ptr(gate_after), _ptr(which), T,
+                                       residual_out.data_ptr(), _ptr(next_in), workspace.data_ptr(), workspace.nbytes,
+                                       _stream_of(residual, stream)))
 
 
 def moe_forward_host(layer, x_host, x_dev, out_host, out_dev, workspace, stream=None):

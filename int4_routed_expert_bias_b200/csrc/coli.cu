@@ -290,10 +290,12 @@ coli_status check_layer_fields(const coli_moe_layer* L, int T)
     if (!std::isfinite(L->routed_scale)) return fail(COLI_ERR_INVALID_ARG, "routed_scale is not finite");
     if (!(L->top_p >= 0.f) || !std::isfinite(L->top_p)) return fail(COLI_ERR_INVALID_ARG, "top_p is negative or not finite");
     if (L->act_int8 != 0 && L->act_int8 != 1) return fail(COLI_ERR_INVALID_ARG, "act_int8=%d (0 or 1)", L->act_int8);
+    // a layer whose routing is always given has no router of its own; check_call asks for it where it is used
     const void* ptrs[] = {L->w_router, L->sel_bias, L->gate_q, L->up_q, L->down_q, L->gate_s, L->up_s, L->down_s};
     const char* names[] = {"w_router", "sel_bias", "gate_q", "up_q", "down_q", "gate_s", "up_s", "down_s"};
     for (int i = 0; i < 8; ++i) {
-        if (!ptrs[i]) return fail(COLI_ERR_INVALID_ARG, "layer.%s is NULL", names[i]);
+        if (!ptrs[i] && (i > 1 || (L->w_router != nullptr) != (L->sel_bias != nullptr)))
+            return fail(COLI_ERR_INVALID_ARG, "layer.%s is NULL", names[i]);
         if (!aligned(ptrs[i], i == 1 ? 4 : 16)) return fail(COLI_ERR_INVALID_ARG, "layer.%s is not 16-byte aligned", names[i]);
     }
     return COLI_OK;
@@ -332,7 +334,7 @@ int lookahead_ranges(const coli_moe_layer* N, const unsigned char** base, unsign
     for (const auto& x : r) {
         const uintptr_t a = reinterpret_cast<uintptr_t>(x.p) + x.off;
         const uintptr_t lo = (a + 15) & ~(uintptr_t)15, hi = (a + x.n) & ~(uintptr_t)15;
-        if (hi <= lo || n == kMaxPrefetch) continue;
+        if (!x.p || hi <= lo || n == kMaxPrefetch) continue;
         base[n] = reinterpret_cast<const unsigned char*>(lo);
         bytes[n] = hi - lo;
         ++n;
@@ -344,10 +346,11 @@ int lookahead_ranges(const coli_moe_layer* N, const unsigned char** base, unsign
 int choose_path(const coli_moe_layer* L, int T);
 
 coli_status check_call(const coli_moe_layer* L, const void* x, coli_dtype xt, int T, const void* out, coli_dtype ot,
-                       const int32_t* topk_idx_out, const float* topk_w_out)
+                       const int32_t* topk_idx_out, const float* topk_w_out, bool given = false)
 {
     coli_status st = check_layer(L, T);
     if (st != COLI_OK) return st;
+    if (!given && !L->w_router) return fail(COLI_ERR_INVALID_ARG, "layer.w_router is NULL");
     if (xt != COLI_F32 && xt != COLI_BF16) return fail(COLI_ERR_INVALID_ARG, "unknown activation dtype %d", (int)xt);
     if (ot != COLI_F32 && ot != COLI_BF16) return fail(COLI_ERR_INVALID_ARG, "unknown output dtype %d", (int)ot);
     if (T == 0) return COLI_OK;
@@ -456,6 +459,20 @@ int choose_path(const coli_moe_layer* L, int T)
 
 }  // namespace
 
+namespace coli {
+
+coli_status check_routed_call(const coli_moe_layer* L, const void* x, coli_dtype xt, int T, const int32_t* topk_idx,
+                              const float* topk_w, const void* out, coli_dtype ot)
+{
+    coli_status st = check_call(L, x, xt, T, out, ot, nullptr, nullptr, true);
+    if (st != COLI_OK || T == 0) return st;
+    if (!topk_idx || !topk_w) return fail(COLI_ERR_INVALID_ARG, "NULL pointer argument");
+    if (!aligned(topk_idx, 4) || !aligned(topk_w, 4)) return fail(COLI_ERR_INVALID_ARG, "routing not 4-byte aligned");
+    return COLI_OK;
+}
+
+}  // namespace coli
+
 extern "C" {
 
 const char* coli_status_string(coli_status st)
@@ -543,9 +560,10 @@ size_t coli_moe_status_word_offset(const coli_moe_layer* L, int T)
     return (size_t)(reinterpret_cast<char*>(w.ctl + 3) - base);
 }
 
-coli_status coli_moe_forward(const coli_moe_layer* L, const void* x, coli_dtype xt, int T, void* out,
-                             coli_dtype ot, void* workspace, size_t ws_bytes, int32_t* topk_idx_out,
-                             float* topk_w_out, cudaStream_t stream)
+// A layer call: routed by the layer's own router, or (given_idx, given_w [T, k]) as the caller says.
+static coli_status run_layer(const coli_moe_layer* L, const void* x, coli_dtype xt, int T, void* out, coli_dtype ot,
+                             void* workspace, size_t ws_bytes, int32_t* topk_idx_out, float* topk_w_out,
+                             const int32_t* given_idx, const float* given_w, cudaStream_t stream)
 {
     StageTimer tm;
     tm.ev = g_prof_events;
@@ -553,7 +571,7 @@ coli_status coli_moe_forward(const coli_moe_layer* L, const void* x, coli_dtype 
     g_prof_events = nullptr;  // one-shot
     g_prof_n = 0;
 
-    coli_status st = check_call(L, x, xt, T, out, ot, topk_idx_out, topk_w_out);
+    coli_status st = check_call(L, x, xt, T, out, ot, topk_idx_out, topk_w_out, given_idx != nullptr);
     if (st != COLI_OK || T == 0) return st;
     if (!workspace) return fail(COLI_ERR_INVALID_ARG, "NULL pointer argument");
     if (!aligned(workspace, 256)) return fail(COLI_ERR_INVALID_ARG, "workspace not 256-byte aligned");
@@ -611,7 +629,7 @@ coli_status coli_moe_forward(const coli_moe_layer* L, const void* x, coli_dtype 
         }
         const bool fused_router = T <= pl.MT;
         if ((e = tm.rec(COLI_STAGE_ROUTE, 0)) != cudaSuccess) return cuda_fail(e, "event record");
-        if (!fused_router) {
+        if (!fused_router && !given_idx) {
             st = launch_logits(x, xt, T, H, L->w_router, E, w.logits, nullptr, 0, stream);
             if (st != COLI_OK) return st;
         }
@@ -619,8 +637,10 @@ coli_status coli_moe_forward(const coli_moe_layer* L, const void* x, coli_dtype 
             (e = tm.rec(COLI_STAGE_UNION, 1)) != cudaSuccess || (e = tm.rec(COLI_STAGE_GATEUP, 0)) != cudaSuccess)
             return cuda_fail(e, "event record");
         LayerArgs la{L->w_router, L->sel_bias, L->gate_q, L->gate_s, L->up_q, L->up_s, L->down_q, L->down_s,
-                     H, F, E, k, T, L->routed_scale, x, out, w.logits, fused_router ? 0 : 1, idx, wt, w.h,
+                     H, F, E, k, T, L->routed_scale, x, out, w.logits, fused_router && !given_idx ? 0 : 1, idx, wt, w.h,
                      w.partial, w.ctl + 3, wait_limit(kBarrierNs), L->top_p, g_stamps.load()};
+        la.given_idx = given_idx;
+        la.given_w = given_w;
         if (pl.out_rows && L->prefetch_next) la.pf_n = lookahead_ranges(L->prefetch_next, la.pf_base, la.pf_bytes);
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(dev->sms);
@@ -664,13 +684,15 @@ coli_status coli_moe_forward(const coli_moe_layer* L, const void* x, coli_dtype 
         return fail(COLI_ERR_CUDA, "cuTensorMapEncodeTiled rejected a prefill tensor map");
     if (path == COLI_PATH_PREFILL) {
         if ((e = tm.rec(COLI_STAGE_ROUTE, 0)) != cudaSuccess) return cuda_fail(e, "event record");
-        {
+        if (!given_idx) {
             dim3 grid((T + kRtT - 1) / kRtT, (E + kRtE - 1) / kRtE);
             if (bf16) router_logits_tiled_kernel<true><<<grid, kRtThreads, 0, stream>>>(x, T, H, L->w_router, E, w.logits);
             else router_logits_tiled_kernel<false><<<grid, kRtThreads, 0, stream>>>(x, T, H, L->w_router, E, w.logits);
         }
-        const bool fused = T <= kFusedTopkMaxT && E <= 256;
-        if (!fused)
+        const bool fused = T <= kFusedTopkMaxT && E <= 256 && !given_idx;
+        if (given_idx)
+            routing_given_kernel<<<(T + 7) / 8, 256, 0, stream>>>(given_idx, given_w, T, E, k, idx, wt);
+        else if (!fused)
             router_topk_kernel<<<(T + 7) / 8, 256, 0, stream>>>(w.logits, T, E, k, L->sel_bias, L->routed_scale, L->top_p, idx, wt);
         if ((e = tm.rec(COLI_STAGE_ROUTE, 1)) != cudaSuccess || (e = tm.rec(COLI_STAGE_UNION, 0)) != cudaSuccess)
             return cuda_fail(e, "event record");
@@ -723,10 +745,14 @@ coli_status coli_moe_forward(const coli_moe_layer* L, const void* x, coli_dtype 
 
     // Route (router scores; the top-k runs in the union block for small batches)
     if ((e = tm.rec(COLI_STAGE_ROUTE, 0)) != cudaSuccess) return cuda_fail(e, "event record");
-    st = launch_logits(x, xt, T, H, L->w_router, E, w.logits, nullptr, 0, stream);
-    if (st != COLI_OK) return st;
-    const bool fused_topk = T <= kFusedTopkMaxT && E <= 256;
-    if (!fused_topk)
+    if (!given_idx) {
+        st = launch_logits(x, xt, T, H, L->w_router, E, w.logits, nullptr, 0, stream);
+        if (st != COLI_OK) return st;
+    }
+    const bool fused_topk = T <= kFusedTopkMaxT && E <= 256 && !given_idx;
+    if (given_idx)
+        routing_given_kernel<<<(T + 7) / 8, 256, 0, stream>>>(given_idx, given_w, T, E, k, idx, wt);
+    else if (!fused_topk)
         router_topk_kernel<<<(T + 7) / 8, 256, 0, stream>>>(w.logits, T, E, k, L->sel_bias, L->routed_scale, L->top_p, idx, wt);
     if ((e = tm.rec(COLI_STAGE_ROUTE, 1)) != cudaSuccess) return cuda_fail(e, "event record");
 
@@ -779,6 +805,26 @@ coli_status coli_moe_forward(const coli_moe_layer* L, const void* x, coli_dtype 
 
     e = cudaGetLastError();
     return e == cudaSuccess ? COLI_OK : cuda_fail(e, "layer launch");
+}
+
+coli_status coli_moe_forward(const coli_moe_layer* L, const void* x, coli_dtype xt, int T, void* out,
+                             coli_dtype ot, void* workspace, size_t ws_bytes, int32_t* topk_idx_out,
+                             float* topk_w_out, cudaStream_t stream)
+{
+    return run_layer(L, x, xt, T, out, ot, workspace, ws_bytes, topk_idx_out, topk_w_out, nullptr, nullptr, stream);
+}
+
+coli_status coli_moe_forward_routed(const coli_moe_layer* L, const void* x, coli_dtype xt, int T, const int32_t* topk_idx,
+                                    const float* topk_w, void* out, coli_dtype ot, void* workspace, size_t ws_bytes,
+                                    cudaStream_t stream)
+{
+    coli_status st = check_routed_call(L, x, xt, T, topk_idx, topk_w, out, ot);
+    if (st != COLI_OK || T == 0) {
+        g_prof_events = nullptr;  // a refused or empty call consumes an armed stage-timing hook too
+        g_prof_n = 0;
+        return st;
+    }
+    return run_layer(L, x, xt, T, out, ot, workspace, ws_bytes, nullptr, nullptr, topk_idx, topk_w, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,126 @@
+// coli_block.cu -- one decoder block around the routed-expert layer
+// (coli_moe_block_forward): the calls of this library in the order a decoder
+// makes them, on one stream and in one workspace.
+#include <algorithm>
+
+#include "coli_common.cuh"
+#include "coli_host.h"
+
+using namespace coli;
+
+namespace {
+
+struct BlockPlan {
+    size_t x, y, idx, w;                  // the layer's input and output, the routing
+    size_t router, layer, adapters;       // workspaces of the calls
+    size_t n_router, n_layer, n_adapters;
+    size_t bytes;
+};
+
+// The fields of a block, and its workspace for T tokens of xt activations.
+coli_status plan_block(const coli_moe_block* b, coli_dtype xt, int T, BlockPlan* p)
+{
+    if (!b) return fail(COLI_ERR_INVALID_ARG, "block is NULL");
+    if (!b->layer || !b->norm_before || !b->norm_after)
+        return fail(COLI_ERR_INVALID_ARG, "block.layer / norm_before / norm_after is NULL");
+    if (!known_dtype(xt)) return fail(COLI_ERR_INVALID_ARG, "unknown activation dtype %d", (int)xt);
+    const int H = b->layer->hidden;
+    if ((p->n_layer = coli_moe_workspace_size(b->layer, T)) == 0) return COLI_ERR_INVALID_ARG;  // described by the call
+    if (b->norm_before->hidden != H || b->norm_after->hidden != H)
+        return fail(COLI_ERR_INVALID_ARG, "block norms of hidden %d / %d around a layer of hidden %d", b->norm_before->hidden,
+                    b->norm_after->hidden, H);
+    if (!b->norm_before->pre_w) return fail(COLI_ERR_INVALID_ARG, "block.norm_before has no pre_w: the layer needs an input");
+    if (b->router) {
+        if ((p->n_router = coli_router_workspace_size(b->router, T)) == 0) return COLI_ERR_INVALID_ARG;
+        if (b->router->hidden != H || b->router->n_experts != b->layer->n_experts || b->router->top_k != b->layer->top_k)
+            return fail(COLI_ERR_INVALID_ARG, "block.router (hidden %d, %d experts, top %d) does not fit the layer",
+                        b->router->hidden, b->router->n_experts, b->router->top_k);
+    } else if (!b->layer->w_router) {
+        return fail(COLI_ERR_INVALID_ARG, "neither block.router nor the layer's own router is given");
+    }
+    if (b->adapters) {
+        if ((p->n_adapters = coli_adapters_workspace_size(b->adapters, T)) == 0) return COLI_ERR_INVALID_ARG;
+        if (b->adapters->in_features != H || b->adapters->out_features != H)
+            return fail(COLI_ERR_INVALID_ARG, "block.adapters are [%d -> %d] beside a layer of hidden %d",
+                        b->adapters->in_features, b->adapters->out_features, H);
+    }
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off += align_up(bytes, 256);
+        return at;
+    };
+    const size_t rows = (size_t)T * H * dtype_size(xt), slots = b->router ? (size_t)T * b->layer->top_k * 4 : 0;
+    p->x = take(rows);
+    p->y = take(rows);
+    p->idx = take(slots);
+    p->w = take(slots);
+    p->router = take(p->n_router);
+    p->layer = take(p->n_layer);
+    p->adapters = take(p->n_adapters);
+    p->bytes = std::max<size_t>(off, 256);
+    return COLI_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t coli_moe_block_workspace_size(const coli_moe_block* b, coli_dtype xt, int T)
+{
+    BlockPlan p{};
+    return plan_block(b, xt, T, &p) == COLI_OK ? p.bytes : 0;
+}
+
+coli_status coli_moe_block_status_word_offsets(const coli_moe_block* b, coli_dtype xt, int T, size_t* router, size_t* layer)
+{
+    BlockPlan p{};
+    coli_status st = plan_block(b, xt, T, &p);
+    if (st != COLI_OK) return st;
+    if (!router || !layer) return fail(COLI_ERR_INVALID_ARG, "NULL pointer argument");
+    *router = b->router && T > 0 ? p.router : SIZE_MAX;
+    const size_t at = coli_moe_status_word_offset(b->layer, T);
+    *layer = at == SIZE_MAX ? SIZE_MAX : p.layer + at;
+    return COLI_OK;
+}
+
+coli_status coli_moe_block_forward(const coli_moe_block* b, const void* prev_out, coli_dtype xt, const void* residual,
+                                   coli_dtype rt, const void* gate_before, const void* gate_after, const int32_t* which,
+                                   int T, void* residual_out, void* next_in, void* workspace, size_t ws_bytes,
+                                   cudaStream_t stream)
+{
+    BlockPlan p{};
+    coli_status st = plan_block(b, xt, T, &p);
+    if (st != COLI_OK) return st;
+    if (!known_dtype(rt)) return fail(COLI_ERR_INVALID_ARG, "unknown residual dtype %d", (int)rt);
+    if (T == 0) return COLI_OK;
+    if (!residual || !residual_out || !workspace) return fail(COLI_ERR_INVALID_ARG, "NULL pointer argument");
+    if (b->adapters && !which) return fail(COLI_ERR_INVALID_ARG, "which is NULL, but the block has adapters");
+    if (b->adapters && !aligned(which, 4)) return fail(COLI_ERR_INVALID_ARG, "which not 4-byte aligned");
+    if (!aligned(workspace, 256)) return fail(COLI_ERR_INVALID_ARG, "workspace not 256-byte aligned");
+    if (ws_bytes < p.bytes) return fail(COLI_ERR_WORKSPACE, "workspace %zu bytes, need %zu", ws_bytes, p.bytes);
+    char* ws = static_cast<char*>(workspace);
+    void *x = ws + p.x, *y = ws + p.y;
+    int32_t* idx = reinterpret_cast<int32_t*>(ws + p.idx);
+    float* w = reinterpret_cast<float*>(ws + p.w);
+    // every step is checked before the first is enqueued
+    if ((st = check_residual_norm(b->norm_before, prev_out, xt, residual, rt, gate_before, T, residual_out, x)) != COLI_OK ||
+        (st = check_routed_call(b->layer, x, xt, T, idx, w, y, xt)) != COLI_OK ||
+        (st = check_residual_norm(b->norm_after, y, xt, residual_out, rt, gate_after, T, residual_out, next_in)) != COLI_OK)
+        return st;
+    if ((st = coli_residual_norm(b->norm_before, prev_out, xt, residual, rt, gate_before, T, residual_out, x, stream)) != COLI_OK)
+        return st;
+    if (b->router) {
+        if ((st = coli_router_forward(b->router, x, xt, T, idx, w, ws + p.router, p.n_router, stream)) != COLI_OK ||
+            (st = coli_moe_forward_routed(b->layer, x, xt, T, idx, w, y, xt, ws + p.layer, p.n_layer, stream)) != COLI_OK)
+            return st;
+    } else if ((st = coli_moe_forward(b->layer, x, xt, T, y, xt, ws + p.layer, p.n_layer, nullptr, nullptr, stream)) != COLI_OK) {
+        return st;
+    }
+    if (b->adapters &&
+        (st = coli_adapters_forward(b->adapters, x, xt, T, which, y, y, xt, ws + p.adapters, p.n_adapters, stream)) != COLI_OK)
+        return st;
+    return coli_residual_norm(b->norm_after, y, xt, residual_out, rt, gate_after, T, residual_out, next_in, stream);
+}
+
+}  // extern "C"

@@ -18,6 +18,13 @@ constexpr int kMaxTokens = 65536;
 coli_status fail(coli_status st, const char* fmt, ...);
 coli_status cuda_fail(cudaError_t e, const char* what);
 
+// Every check of these calls apart from the workspace, for callers that run
+// several of them and must refuse before the first launch.
+coli_status check_routed_call(const coli_moe_layer* layer, const void* x, coli_dtype xt, int T, const int32_t* topk_idx,
+                              const float* topk_w, const void* out, coli_dtype ot);
+coli_status check_residual_norm(const coli_block_norm* norm, const void* block_out, coli_dtype xt, const void* residual,
+                                coli_dtype rt, const void* gate, int T, void* residual_out, void* normed_out);
+
 // The limit of the kernels' bounded waits: the test hook's value if set, else dflt.
 unsigned long long wait_limit(unsigned long long dflt);
 

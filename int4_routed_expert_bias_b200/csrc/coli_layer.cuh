@@ -398,6 +398,9 @@ struct LayerArgs {
     const unsigned char* pf_base[kMaxPrefetch];
     unsigned long long pf_bytes[kMaxPrefetch];
     int pf_n;
+    // routing given by the caller [T, k] (n_pieces = 1, nothing is scored), or null
+    const int32_t* given_idx;
+    const float* given_w;
 };
 
 constexpr int kStamps = 16;
@@ -1117,7 +1120,7 @@ moe_layer_kernel(const LayerArgs a, const LayerSmem ls)
             // the token's router scores (sums of the pieces), sigmoids and selection keys
             uint32_t* s_key = reinterpret_cast<uint32_t*>(u.mask);  // the union's token masks are not used here
             float* s_sig = reinterpret_cast<float*>(u.mask) + E;
-            for (int e = threadIdx.x; e < E; e += kLayerThreads) {
+            for (int e = a.given_idx ? E : threadIdx.x; e < E; e += kLayerThreads) {
                 float v = 0.f;
 #pragma unroll
                 for (int p = 0; p < 16; ++p)
@@ -1135,8 +1138,12 @@ moe_layer_kernel(const LayerArgs a, const LayerSmem ls)
                 // the token's top-k, then the union of its k experts: ascending expert order
                 int my_e;
                 float my_s, my_w;
-                topk_smem(s_key, s_sig, E, k, my_e, my_s);
-                topk_weights(k, a.top_p, a.routed_scale, my_e, my_s, my_w);
+                if (a.given_idx) {
+                    given_slot(a.given_idx, a.given_w, E, k, my_e, my_w);
+                } else {
+                    topk_smem(s_key, s_sig, E, k, my_e, my_s);
+                    topk_weights(k, a.top_p, a.routed_scale, my_e, my_s, my_w);
+                }
                 // kept experts (top-p may drop slots: expert -1) in ascending order
                 int rank = 0;
                 for (int i = 0; i < k; ++i) {
@@ -1209,7 +1216,7 @@ moe_layer_kernel(const LayerArgs a, const LayerSmem ls)
         stream_rows<MT, kRW, P_GU, nd>(first, kLayerWarps, nj, gH.per_lane, gH.nch, xs, xcorr, ring, rows_of, vecs_of,
                                        fin);
     } else {
-        const bool scored_here = all_x;  // the kernel scored the tokens (npc partial pieces per score)
+        const bool scored_here = all_x && !a.given_idx;  // the kernel scored the tokens (npc partial pieces per score)
         if (scored_here) {
             // the scores: sums of the pieces (independent loads, every thread), into shared memory
             for (int i = threadIdx.x; i < T * E; i += kLayerThreads) {
@@ -1225,7 +1232,9 @@ moe_layer_kernel(const LayerArgs a, const LayerSmem ls)
         for (int t = warp; t < T; t += kLayerWarps) {
             int my_e;
             float my_w;
-            if (E <= 256) {
+            if (a.given_idx) {
+                given_slot(a.given_idx + (size_t)t * k, a.given_w + (size_t)t * k, E, k, my_e, my_w);
+            } else if (E <= 256) {
                 float l[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {

@@ -45,9 +45,8 @@ coli_status check_norm(const coli_block_norm* n)
 
 }  // namespace
 
-extern "C" coli_status coli_residual_norm(const coli_block_norm* n, const void* block_out, coli_dtype xt,
-                                          const void* residual, coli_dtype rt, const void* gate, int T,
-                                          void* residual_out, void* normed_out, cudaStream_t stream)
+coli_status coli::check_residual_norm(const coli_block_norm* n, const void* block_out, coli_dtype xt, const void* residual,
+                                      coli_dtype rt, const void* gate, int T, void* residual_out, void* normed_out)
 {
     coli_status st = check_norm(n);
     if (st != COLI_OK) return st;
@@ -87,7 +86,15 @@ extern "C" coli_status coli_residual_norm(const coli_block_norm* n, const void* 
             return fail(COLI_ERR_INVALID_ARG, "normed_out overlaps an input without being the same tensor");
     }
     if (overlap(residual_out, nr, normed_out, nx)) return fail(COLI_ERR_INVALID_ARG, "residual_out and normed_out overlap");
+    return COLI_OK;
+}
 
+extern "C" coli_status coli_residual_norm(const coli_block_norm* n, const void* block_out, coli_dtype xt,
+                                          const void* residual, coli_dtype rt, const void* gate, int T,
+                                          void* residual_out, void* normed_out, cudaStream_t stream)
+{
+    coli_status st = check_residual_norm(n, block_out, xt, residual, rt, gate, T, residual_out, normed_out);
+    if (st != COLI_OK || T == 0) return st;
     NormArgs a{};
     a.T = T, a.H = n->hidden;
     a.eps = n->eps, a.inv_h = 1.0f / (float)n->hidden;

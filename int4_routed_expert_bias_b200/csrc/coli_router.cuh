@@ -196,6 +196,44 @@ __device__ __forceinline__ void topk_weights(int k, float top_p, float routed_sc
     if (lane < k && !keep) my_e = -1;
 }
 
+// Slot `lane` of a token's given routing, by one warp: an index outside [0, E) is a
+// dropped slot (-1, weight 0); an expert named twice keeps its first slot with
+// the sum of its weights (the same output), the other slots are dropped.
+__device__ __forceinline__ void given_slot(const int32_t* __restrict__ idx_row, const float* __restrict__ w_row, int E, int k,
+                                           int& my_e, float& my_w)
+{
+    const int lane = threadIdx.x & 31;
+    int e = lane < k ? idx_row[lane] : -1;
+    if (e < 0 || e >= E) e = -1;
+    const float w = e >= 0 ? w_row[lane] : 0.f;
+    my_e = e;
+    my_w = w;
+    for (int i = 0; i < k; ++i) {
+        const int ei = __shfl_sync(0xFFFFFFFFu, e, i);
+        const float wi = __shfl_sync(0xFFFFFFFFu, w, i);
+        if (e >= 0 && ei == e) {
+            if (i < lane) my_e = -1, my_w = 0.f;
+            else if (i > lane && my_e >= 0) my_w += wi;
+        }
+    }
+}
+
+// A given routing [T, k] brought into the form the union expects, one warp per token.
+__global__ void __launch_bounds__(256)
+routing_given_kernel(const int32_t* __restrict__ idx, const float* __restrict__ w, int T, int E, int k,
+                     int32_t* __restrict__ idx_out, float* __restrict__ w_out)
+{
+    const int t = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
+    if (t >= T) return;  // whole warp leaves together
+    int e;
+    float v;
+    given_slot(idx + (size_t)t * k, w + (size_t)t * k, E, k, e, v);
+    if (lane < k) {
+        idx_out[(size_t)t * k + lane] = e;
+        w_out[(size_t)t * k + lane] = v;
+    }
+}
+
 // Top-k of one token by one warp: sigmoid, bias, k rounds of warp arg-max,
 // renormalised weights.  Lane j keeps the j-th selection.  The arg-max key is
 // (c desc, index asc); a non-finite score can never make the warp pick an index
