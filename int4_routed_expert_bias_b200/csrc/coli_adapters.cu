@@ -34,10 +34,15 @@ struct LoPlan {
     size_t perm, tiles, n_tiles, bytes;  // workspace offsets (partial sums of h first)
 };
 
+size_t expand_smem(int R, coli_dtype ot)
+{
+    return (size_t)(ot == COLI_BF16 ? 2 : 3) * kLoTile * ((R + 31) / 32 * 32 + 8) * 2;
+}
+
 LoPlan lo_plan(const coli_adapters* d, int T)
 {
     LoPlan p{};
-    // tiles of T tokens over g groups: at most T / 32 whole ones and one more per group
+    // tiles of T tokens over g groups: at most T / 64 whole ones and one more per group
     p.max_tiles = std::max(1, T / kLoTile + std::min(T, d->n_adapters + 1));
     // pieces of K that give about two blocks per SM, each with at least one 32-K block for every warp
     const int most = std::max(1, d->in_features / (32 * kLoWarps));
@@ -102,21 +107,20 @@ coli_status coli_adapters_forward(const coli_adapters* d, const void* x, coli_dt
     cudaError_t e = cudaSuccess;
     const dim3 g1(p.max_tiles, p.pieces), g2(p.max_tiles, (a.N + a.cols - 1) / a.cols);
     if (T > kLoSmallT) {
-        lo_group_kernel<<<1, kLoGroupThreads, 0, stream>>>(a);
-        if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "adapter grouping launch");
-        e = launch_pdl(xt == COLI_BF16 ? lo_shrink_kernel<true> : lo_shrink_kernel<false>, g1, kLoThreads, 0, stream, a);
-    } else {
-        if (xt == COLI_BF16) lo_shrink_kernel<true><<<g1, kLoThreads, 0, stream>>>(a);
-        else lo_shrink_kernel<false><<<g1, kLoThreads, 0, stream>>>(a);
-        e = cudaGetLastError();
+        if ((e = launch_pdl(lo_group_kernel, dim3(1), kLoGroupThreads, 0, stream, a)) != cudaSuccess)
+            return cuda_fail(e, "adapter grouping launch");
     }
+    if ((st = xt == COLI_BF16 ? allow_smem_once<lo_shrink_kernel<true>>((int)LoShrink<true>::kSmem)
+                              : allow_smem_once<lo_shrink_kernel<false>>((int)LoShrink<false>::kSmem)) != COLI_OK ||
+        (st = ot == COLI_BF16 ? allow_smem_once<lo_expand_kernel<true>>((int)expand_smem(kLoMaxRank, ot))
+                              : allow_smem_once<lo_expand_kernel<false>>((int)expand_smem(kLoMaxRank, ot))) != COLI_OK)
+        return st;
+    e = xt == COLI_BF16 ? launch_pdl(lo_shrink_kernel<true>, g1, kLoThreads, LoShrink<true>::kSmem, stream, a)
+                        : launch_pdl(lo_shrink_kernel<false>, g1, kLoThreads, LoShrink<false>::kSmem, stream, a);
     if (e != cudaSuccess) return cuda_fail(e, "adapter shrink launch");
-    const size_t rs = (size_t)(a.R + 31) / 32 * 32 + 8;
-    const size_t smem = (ot == COLI_BF16 ? 2 : 3) * kLoTile * rs * 2;
-    auto kern = ot == COLI_BF16 ? lo_expand_kernel<true> : lo_expand_kernel<false>;
-    if (smem > 46 * 1024 && (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
-        return cuda_fail(e, "kernel attribute setup");
-    e = launch_pdl(kern, g2, kLoThreads, smem, stream, a);
+    const size_t smem = expand_smem(a.R, ot);
+    e = ot == COLI_BF16 ? launch_pdl(lo_expand_kernel<true>, g2, kLoThreads, smem, stream, a)
+                        : launch_pdl(lo_expand_kernel<false>, g2, kLoThreads, smem, stream, a);
     return e == cudaSuccess ? COLI_OK : cuda_fail(e, "adapter expand launch");
 }
 

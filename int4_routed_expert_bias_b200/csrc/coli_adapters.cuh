@@ -3,13 +3,18 @@
 //   out_t = base_t + scale_a B_a (A_a x_t),  a = the adapter of token t
 // A_a is [rank, K], B_a is [N, rank], bf16; tokens without an adapter keep base.
 //
-// Tokens are grouped into tiles of up to 32 of one adapter, so each adapter is
+// Tokens are grouped into tiles of up to 64 of one adapter, so each adapter is
 // read once per tile.  Two kernels:
-//   shrink   h = A_a x for (tile, piece of K): eight warps take 32-K blocks,
-//            their sums meet in shared memory, one fp32 partial row per piece
+//   shrink   h = A_a x for (tile, piece of K): the warps take 32-K blocks, their
+//            sums meet in shared memory, one fp32 partial row per piece
 //   expand   out for (tile, columns): the pieces of h are summed in order, scaled,
 //            cut into bf16 parts; each warp multiplies them with 32 rows of B_a at
 //            a time and adds base
+// A warp works on 32 tokens; in a tile of more, pairs of warps share the adapter's
+// rows (the second read finds them in L1).  The expand kernel starts while the
+// shrink kernel runs and has its first rows of B and base on the way before it
+// waits for h.
+//
 // Memory-bound: at 4096 tokens, K = N = 6144, rank 64 the arithmetic is 6.4 GFLOP
 // against 176 MB, 4 us of tensor work beside 27 us of traffic, so the products run
 // on warp-level mma (m16n8k16, fp32 accumulation) whose operands come straight
@@ -27,12 +32,12 @@
 
 namespace coli {
 
-constexpr int kLoTile = 32;      // tokens per tile
+constexpr int kLoTile = 64;      // tokens per tile
+constexpr int kLoRows = 32;      // tokens of a warp
 constexpr int kLoThreads = 256;
 constexpr int kLoWarps = kLoThreads / 32;
 constexpr int kLoMaxRank = 256;
-constexpr int kLoRB = 64;        // rank values accumulated at a time in the shrink kernel
-constexpr int kLoSmallT = 64;    // batches up to this size are grouped inside each block
+constexpr int kLoSmallT = 64;    // batches up to this size are grouped inside each block: one tile per adapter
 constexpr int kLoGroupThreads = 1024;
 
 struct LoArgs {
@@ -71,8 +76,10 @@ __global__ void __launch_bounds__(kLoGroupThreads) lo_group_kernel(const __grid_
     __shared__ int wsum[2][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, bins = a.n + 1;
     for (int i = threadIdx.x; i < bins; i += kLoGroupThreads) count[i] = 0;
-    __syncthreads();
+    griddep_wait();
     griddep_launch_dependents();
+    __syncthreads();
+#pragma unroll 4
     for (int t0 = warp * 32; t0 < a.T; t0 += kLoGroupThreads) {
         const int t = t0 + lane;
         const int w = t < a.T ? lo_adapter(a, t) : -1;
@@ -112,6 +119,7 @@ __global__ void __launch_bounds__(kLoGroupThreads) lo_group_kernel(const __grid_
         __syncthreads();
     }
     if (threadIdx.x == 0) *a.n_tiles = base_t;
+#pragma unroll 4
     for (int t0 = warp * 32; t0 < a.T; t0 += kLoGroupThreads) {
         const int t = t0 + lane;
         const int w = t < a.T ? lo_adapter(a, t) : -1;
@@ -124,16 +132,17 @@ __global__ void __launch_bounds__(kLoGroupThreads) lo_group_kernel(const __grid_
     }
 }
 
-// The tile of a block: its adapter and tokens.  Shared memory of the two kernels.
+// The tile of a block: its adapter and tokens.
 struct LoTile {
     int adapter, count;
     int token[kLoTile];
-    int of[kLoSmallT], start[kLoSmallT];  // grouping of a small batch
+    int of[kLoSmallT];       // grouping of a small batch
+    uint32_t leaders[2];
 };
 
 // Fills `s` for tile number `tile`; false when there is no such tile.  Small
-// batches are grouped here, by first token of each adapter; large ones were
-// grouped by lo_group_kernel.  All threads call it.
+// batches are grouped here, one tile per adapter in order of its first token;
+// large ones were grouped by lo_group_kernel.  All threads call it.
 __device__ __forceinline__ bool lo_find_tile(const LoArgs& a, int tile, LoTile& s)
 {
     const int tid = threadIdx.x;
@@ -145,36 +154,32 @@ __device__ __forceinline__ bool lo_find_tile(const LoArgs& a, int tile, LoTile& 
         __syncthreads();
         return true;
     }
-    if (tid == 0) s.count = 0;
     int w = -1;
     if (tid < kLoSmallT) s.of[tid] = w = tid < a.T ? lo_adapter(a, tid) : -1;
     __syncthreads();
-    int cnt = 0, pos = 0, lead = 0;
-    if (tid < a.T) {
-        for (int i = a.T - 1; i >= 0; --i) {
-            const bool same = s.of[i] == w;
-            cnt += same ? 1 : 0;
-            pos += same && i < tid ? 1 : 0;
-            if (same) lead = i;
-        }
-        s.start[tid] = pos == 0 ? (cnt + kLoTile - 1) / kLoTile : 0;
+    unsigned long long same = 0;
+    if (tid < kLoSmallT) {  // two whole warps
+#pragma unroll
+        for (int i = 0; i < kLoSmallT; ++i) same |= s.of[i] == w ? 1ull << i : 0ull;
+        const bool leads = tid < a.T && __ffsll(same) - 1 == tid;
+        const uint32_t m = __ballot_sync(0xFFFFFFFFu, leads);
+        if ((tid & 31) == 0) s.leaders[tid >> 5] = m;
     }
     __syncthreads();
+    const unsigned long long leaders = s.leaders[0] | (unsigned long long)s.leaders[1] << 32;
+    if (tile >= __popcll(leaders)) return false;
     if (tid < a.T) {
-        int t0 = 0;  // first tile of this token's adapter
-        for (int i = 0; i < lead; ++i) t0 += s.start[i];
-        if (t0 + pos / kLoTile == tile) {
-            s.token[pos % kLoTile] = tid;
-            if (pos % kLoTile == 0) {
+        const int lead = __ffsll(same) - 1;
+        if (__popcll(leaders & ((1ull << lead) - 1ull)) == tile) {
+            const int pos = __popcll(same & ((1ull << tid) - 1ull)), cnt = __popcll(same);
+            s.token[pos] = tid;
+            if (pos == 0) {
                 s.adapter = w;
-                s.count = min(kLoTile, cnt - pos);
+                s.count = cnt;
+                for (int i = cnt; i < kLoTile; ++i) s.token[i] = tid;  // the tail repeats a token
             }
         }
     }
-    __syncthreads();
-    const int c = s.count;
-    if (c == 0) return false;
-    if (tid >= c && tid < kLoTile) s.token[tid] = s.token[0];
     __syncthreads();
     return true;
 }
@@ -197,114 +202,146 @@ __device__ __forceinline__ uint32_t cut_pair(float& lo, float& hi)
     return w;
 }
 
-// h[t, r] of one piece of K.  Grid (tiles, pieces).
+// h[t, r] of one piece of K.  Grid (tiles, pieces).  Two blocks per SM keep about
+// 100 KB of loads under way on each.  kRB: rank values accumulated at a time (the
+// three parts of fp32 x leave registers for half as many).
+// K is always cut into eight shares (32-K block i belongs to share i mod 8), summed
+// pairwise in the same order, so a token's sums do not depend on how many share
+// its tile: with one set of 32 tokens every warp takes a share, with two sets a
+// warp takes share w + 4, puts it aside in shared memory, and then share w.
 template <bool kX16>
-__global__ void __launch_bounds__(kLoThreads) lo_shrink_kernel(const __grid_constant__ LoArgs a)
+struct LoShrink {
+    static constexpr int kRB = kX16 ? 64 : 32;
+    static constexpr int kSlot = kLoRows * kRB;                        // floats of one warp's sums
+    static constexpr size_t kSmem = (size_t)kLoWarps * kSlot * 4;
+};
+
+template <bool kX16>
+__global__ void __launch_bounds__(kLoThreads, 2) lo_shrink_kernel(const __grid_constant__ LoArgs a)
 {
-    constexpr int kParts = kX16 ? 1 : 3;
+    constexpr int kParts = kX16 ? 1 : 3, kRB = LoShrink<kX16>::kRB, kJ = kRB / 8, kSlot = LoShrink<kX16>::kSlot;
     __shared__ LoTile s;
-    __shared__ __align__(16) float sum[kLoWarps / 2][kLoTile * kLoRB];
+    extern __shared__ __align__(16) float sum[];  // [kLoWarps][kSlot]
     griddep_wait();
     griddep_launch_dependents();
     if (!lo_find_tile(a, blockIdx.x, s) || s.adapter == a.n) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const int ad = s.adapter, rank = a.rank ? min(max(a.rank[ad], 0), a.R) : a.R;
-    const bool two = s.count > 16;  // a second 16-row half
+    const int sets = s.count > kLoRows ? 2 : 1;
+    const int set = sets == 2 ? warp & 1 : 0, wk = sets == 2 ? warp >> 1 : warp;
+    const int row0 = set * kLoRows + g, left = s.count - set * kLoRows;
+    const bool two = left > 16;  // a second half of 16 tokens
     const int k0 = blockIdx.y * a.chunk, k1 = min(a.K, k0 + a.chunk);
     const size_t es = kX16 ? 2 : 4;
     const char* xr[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) xr[i] = static_cast<const char*>(a.x) + ((size_t)s.token[g + 8 * i] * a.K + 8 * q) * es;
-    for (int r0 = 0; r0 < rank; r0 += kLoRB) {
-        const int nt = min(kLoRB / 8, (rank - r0 + 7) / 8);
+    for (int i = 0; i < 4; ++i) xr[i] = static_cast<const char*>(a.x) + ((size_t)s.token[row0 + 8 * i] * a.K + 8 * q) * es;
+    for (int r0 = 0; r0 < rank; r0 += kRB) {
+        const int nt = min(kJ, (rank - r0 + 7) / 8);
         const uint16_t* ap = a.a + ((size_t)ad * a.R + r0 + g) * a.K + 8 * q;
-        float acc[2][kLoRB / 8][4];
+        float acc[2][kJ][4];
+        auto put = [&](int slot) {
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int j = 0; j < kLoRB / 8; ++j)
+                for (int j = 0; j < kJ; ++j)
+                    if (j < nt && (m == 0 || two))
+                        *reinterpret_cast<float4*>(&sum[slot * kSlot + ((m * kJ + j) * 32 + lane) * 4]) =
+                            make_float4(acc[m][j][0], acc[m][j][1], acc[m][j][2], acc[m][j][3]);
+        };
+        auto add = [&](int slot) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) acc[m][j][c] = 0.f;
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int j = 0; j < kJ; ++j)
+                    if (j < nt && (m == 0 || two)) {
+                        const float4 o = *reinterpret_cast<const float4*>(&sum[slot * kSlot + ((m * kJ + j) * 32 + lane) * 4]);
+                        acc[m][j][0] += o.x, acc[m][j][1] += o.y, acc[m][j][2] += o.z, acc[m][j][3] += o.w;
+                    }
+        };
 #pragma unroll 1
-        for (int k = k0 + 32 * warp; k < k1; k += 32 * kLoWarps) {
-            const bool in = k + 8 * q < a.K;  // K is a multiple of 8: whole lanes end
-            uint4 w[kLoRB / 8];
+        for (int share = wk + (sets == 2 ? kLoWarps / 2 : 0); share >= 0; share -= kLoWarps / 2) {
+            if (share < wk) break;
 #pragma unroll
-            for (int j = 0; j < kLoRB / 8; ++j) {
-                w[j] = make_uint4(0u, 0u, 0u, 0u);
-                if (in && j < nt && r0 + 8 * j + g < rank) w[j] = *reinterpret_cast<const uint4*>(ap + (size_t)8 * j * a.K + k);
-            }
-            uint4 xv[4][kX16 ? 1 : 2];
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+                for (int j = 0; j < kJ; ++j)
 #pragma unroll
-                for (int v = 0; v < (kX16 ? 1 : 2); ++v) {
-                    xv[i][v] = make_uint4(0u, 0u, 0u, 0u);
-                    if (in && (i < 2 || two)) xv[i][v] = *reinterpret_cast<const uint4*>(xr[i] + (size_t)k * es + 16 * v);
+                    for (int c = 0; c < 4; ++c) acc[m][j][c] = 0.f;
+#pragma unroll 1
+            for (int k = k0 + 32 * share; k < k1; k += 32 * kLoWarps) {
+                const bool in = k + 8 * q < a.K;  // K is a multiple of 8: whole lanes end
+                uint4 xv[4][kX16 ? 1 : 2];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int v = 0; v < (kX16 ? 1 : 2); ++v) {
+                        xv[i][v] = make_uint4(0u, 0u, 0u, 0u);
+                        if (in && (i < 2 || two)) xv[i][v] = *reinterpret_cast<const uint4*>(xr[i] + (size_t)k * es + 16 * v);
+                    }
+                uint4 w[kJ];
+#pragma unroll
+                for (int j = 0; j < kJ; ++j) {
+                    w[j] = make_uint4(0u, 0u, 0u, 0u);
+                    if (in && j < nt && r0 + 8 * j + g < rank) w[j] = *reinterpret_cast<const uint4*>(ap + (size_t)8 * j * a.K + k);
                 }
-            // parts of x: four bf16 pairs per row and part, pairs 0, 1 for the first MMA, 2, 3 for the second
-            uint32_t p[kParts][4][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (kX16) {
-                    p[0][i][0] = xv[i][0].x, p[0][i][1] = xv[i][0].y, p[0][i][2] = xv[i][0].z, p[0][i][3] = xv[i][0].w;
-                } else {
-                    float f[8] = {__uint_as_float(xv[i][0].x), __uint_as_float(xv[i][0].y), __uint_as_float(xv[i][0].z),
-                                  __uint_as_float(xv[i][0].w), __uint_as_float(xv[i][1].x), __uint_as_float(xv[i][1].y),
-                                  __uint_as_float(xv[i][1].z), __uint_as_float(xv[i][1].w)};
+                for (int m = 0; m < 2; ++m) {
+                    if (m == 1 && !two) break;
+                    // parts of two rows of x: four bf16 pairs each, pairs 0, 1 for the first MMA, 2, 3 for the second
+                    uint32_t p[kParts][2][4];
 #pragma unroll
-                    for (int u = 0; u < kParts; ++u)
+                    for (int i = 0; i < 2; ++i) {
+                        const uint4 u0 = xv[2 * m + i][0];
+                        if constexpr (kX16) {
+                            p[0][i][0] = u0.x, p[0][i][1] = u0.y, p[0][i][2] = u0.z, p[0][i][3] = u0.w;
+                        } else {
+                            const uint4 u1 = xv[2 * m + i][1];
+                            float f[8] = {__uint_as_float(u0.x), __uint_as_float(u0.y), __uint_as_float(u0.z), __uint_as_float(u0.w),
+                                          __uint_as_float(u1.x), __uint_as_float(u1.y), __uint_as_float(u1.z), __uint_as_float(u1.w)};
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) p[u][i][c] = cut_pair(f[2 * c], f[2 * c + 1]);
-                }
-            }
+                            for (int u = 0; u < kParts; ++u)
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                if (m == 1 && !two) break;
+                                for (int c = 0; c < 4; ++c) p[u][i][c] = cut_pair(f[2 * c], f[2 * c + 1]);
+                        }
+                    }
 #pragma unroll
-                for (int j = 0; j < kLoRB / 8; ++j) {
-                    if (j >= nt) break;
+                    for (int j = 0; j < kJ; ++j) {
+                        if (j >= nt) break;
 #pragma unroll
-                    for (int u = kParts - 1; u >= 0; --u) {  // small parts first
-                        mma_bf16(acc[m][j], p[u][2 * m][0], p[u][2 * m + 1][0], p[u][2 * m][1], p[u][2 * m + 1][1], w[j].x, w[j].y);
-                        mma_bf16(acc[m][j], p[u][2 * m][2], p[u][2 * m + 1][2], p[u][2 * m][3], p[u][2 * m + 1][3], w[j].z, w[j].w);
+                        for (int u = kParts - 1; u >= 0; --u) {  // small parts first
+                            mma_bf16(acc[m][j], p[u][0][0], p[u][1][0], p[u][0][1], p[u][1][1], w[j].x, w[j].y);
+                            mma_bf16(acc[m][j], p[u][0][2], p[u][1][2], p[u][0][3], p[u][1][3], w[j].z, w[j].w);
+                        }
                     }
                 }
             }
+            if (share != wk) put(warp);
         }
-        // sum of the warps: the upper half hands its sums to the lower, three times
-#pragma unroll
-        for (int half = kLoWarps / 2; half > 0; half >>= 1) {
+        // pairwise sums of the shares: w and w + 4, then w and w + 2, then w and w + 1
+        if (sets == 2) {
+            add(warp);
+        } else {
             __syncthreads();
-            if (warp >= half && warp < 2 * half) {
-#pragma unroll
-                for (int m = 0; m < 2; ++m)
-#pragma unroll
-                    for (int j = 0; j < kLoRB / 8; ++j)
-                        if (j < nt && (m == 0 || two))
-                            *reinterpret_cast<float4*>(&sum[warp - half][((m * (kLoRB / 8) + j) * 32 + lane) * 4]) =
-                                make_float4(acc[m][j][0], acc[m][j][1], acc[m][j][2], acc[m][j][3]);
-            }
+            if (wk >= 4) put(wk);
             __syncthreads();
-            if (warp < half) {
-#pragma unroll
-                for (int m = 0; m < 2; ++m)
-#pragma unroll
-                    for (int j = 0; j < kLoRB / 8; ++j)
-                        if (j < nt && (m == 0 || two)) {
-                            const float4 o =
-                                *reinterpret_cast<const float4*>(&sum[warp][((m * (kLoRB / 8) + j) * 32 + lane) * 4]);
-                            acc[m][j][0] += o.x, acc[m][j][1] += o.y, acc[m][j][2] += o.z, acc[m][j][3] += o.w;
-                        }
-            }
+            if (wk < 4) add(wk + 4);
         }
-        if (warp == 0) {
+#pragma unroll 1
+        for (int half = 2; half > 0; half >>= 1) {
+            __syncthreads();
+            if (wk >= half && wk < 2 * half) put(set * 4 + wk);
+            __syncthreads();
+            if (wk < half) add(set * 4 + wk + half);
+        }
+        __syncthreads();
+        if (wk == 0) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                if (g + 8 * i >= s.count) continue;
-                float* hp = a.h + ((size_t)blockIdx.y * a.T + s.token[g + 8 * i]) * a.R + r0 + 2 * q;
+                if (g + 8 * i >= left) continue;
+                float* hp = a.h + ((size_t)blockIdx.y * a.T + s.token[row0 + 8 * i]) * a.R + r0 + 2 * q;
 #pragma unroll
-                for (int j = 0; j < kLoRB / 8; ++j)
+                for (int j = 0; j < kJ; ++j)
                     if (j < nt) {
                         const float* c = &acc[i >> 1][j][(i & 1) * 2];
                         *reinterpret_cast<float2*>(hp + 8 * j) = make_float2(c[0], c[1]);
@@ -315,65 +352,98 @@ __global__ void __launch_bounds__(kLoThreads) lo_shrink_kernel(const __grid_cons
 }
 
 // out = base + (scale h) B^T for a tile and `cols` columns.  Grid (tiles, column blocks).
-// Shared memory: the parts of scale h, [kParts][32][rs] bf16, rs = R rounded to 32, + 8 (rows on other banks).
+// Shared memory: the parts of scale h, [kParts][64][rs] bf16, rs = R rounded to 32, + 8 (rows on other banks).
 template <bool kO16>
-__global__ void __launch_bounds__(kLoThreads) lo_expand_kernel(const __grid_constant__ LoArgs a)
+__global__ void __launch_bounds__(kLoThreads, 2) lo_expand_kernel(const __grid_constant__ LoArgs a)
 {
-    constexpr int kParts = kO16 ? 2 : 3;
+    constexpr int kParts = kO16 ? 2 : 3, kV = kO16 ? 1 : 2;
     extern __shared__ __align__(16) uint16_t hs[];
     __shared__ LoTile s;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    griddep_wait();
-    if (!lo_find_tile(a, blockIdx.x, s)) return;
+    // Everything but h was complete before the shrink kernel let this one start.
+    const bool found = lo_find_tile(a, blockIdx.x, s);
+    if (!found || (s.adapter == a.n && a.base == a.out)) {  // in place: nothing to add
+        griddep_wait();
+        return;
+    }
     const int ad = s.adapter;
-    if (ad == a.n && a.base == a.out) return;  // in place: nothing to add
     const int rank = ad == a.n ? 0 : a.rank ? min(max(a.rank[ad], 0), a.R) : a.R;
     const int rp = (rank + 31) / 32 * 32, rs = (a.R + 31) / 32 * 32 + 8;
-    const bool two = s.count > 16;
+    const int sets = s.count > kLoRows ? 2 : 1, nw = kLoWarps / sets;
+    const int set = sets == 2 ? warp & 1 : 0, wn = sets == 2 ? warp >> 1 : warp;
+    const int row0 = set * kLoRows + g, left = s.count - set * kLoRows;
+    const bool two = left > 16;
+    const int c_end = min(a.N, (int)(blockIdx.y + 1) * a.cols);
+
+    uint4 bv[4][kV], w[2][4];
+    // base of 32 columns: this lane's 8 (N is a multiple of 8) of four rows
+    auto load_base = [&](int n0) {
+        const int col = n0 + 8 * q;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int v = 0; v < kV; ++v) {
+                bv[i][v] = make_uint4(0u, 0u, 0u, 0u);
+                if (a.base && col < a.N && g + 8 * i < left)
+                    bv[i][v] = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.base) +
+                                                               ((size_t)s.token[row0 + 8 * i] * a.N + col) * (kO16 ? 2 : 4) + 16 * v);
+            }
+    };
+    // rows of B for 32 columns and 64 rank values.  Column g of MMA j is output column
+    // n0 + 8 (g / 2) + 2 j + g % 2, so that lane q's results are columns 8 q + 0..7.
+    auto load_b = [&](int n0, int r) {
+        const int brow = n0 + 8 * (g >> 1) + (g & 1);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int rr = r + 32 * h + 8 * q;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                w[h][j] = make_uint4(0u, 0u, 0u, 0u);
+                if (brow + 2 * j < a.N && rr < rank)
+                    w[h][j] = *reinterpret_cast<const uint4*>(a.b + ((size_t)ad * a.N + brow + 2 * j) * a.R + rr);
+            }
+        }
+    };
+    int n0 = blockIdx.y * a.cols + 32 * wn;
+    if (n0 < c_end) {
+        load_base(n0);
+        load_b(n0, 0);
+    }
+    const float scale = rank > 0 ? a.scale[ad] : 0.f;
+    griddep_wait();
     if (rank > 0) {
-        const float scale = a.scale[ad];
         const size_t plane = (size_t)a.T * a.R;
-        for (int i = threadIdx.x; i < kLoTile * (rp / 2); i += kLoThreads) {
+        for (int i = threadIdx.x; i < kLoRows * sets * (rp / 2); i += kLoThreads) {
             const int row = i / (rp / 2), r = 2 * (i - row * (rp / 2));
             float v0 = 0.f, v1 = 0.f;
             if (row < s.count && r < rank) {  // R is even, so a pair is inside the row
                 const float* hp = a.h + (size_t)s.token[row] * a.R + r;
-                for (int p = 0; p < a.pieces; ++p) {
-                    const float2 o = *reinterpret_cast<const float2*>(hp + p * plane);
-                    v0 += o.x, v1 += o.y;
+                for (int p0 = 0; p0 < a.pieces; p0 += 8) {  // eight independent loads at a time
+                    float2 o[8];
+#pragma unroll
+                    for (int p = 0; p < 8; ++p)
+                        o[p] = p0 + p < a.pieces ? *reinterpret_cast<const float2*>(hp + (p0 + p) * plane) : make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int p = 0; p < 8; ++p) v0 += o[p].x, v1 += o[p].y;
                 }
                 v0 *= scale;
                 v1 = r + 1 < rank ? v1 * scale : 0.f;
             }
 #pragma unroll
             for (int u = 0; u < kParts; ++u) {
-                uint32_t w;
+                uint32_t e;
                 if (kO16 && u == kParts - 1) {  // the last of two parts is rounded, not cut
                     const __nv_bfloat162 v = __floats2bfloat162_rn(v0, v1);
-                    w = *reinterpret_cast<const uint32_t*>(&v);
+                    e = *reinterpret_cast<const uint32_t*>(&v);
                 } else {
-                    w = cut_pair(v0, v1);
+                    e = cut_pair(v0, v1);
                 }
-                *reinterpret_cast<uint32_t*>(hs + (size_t)(u * kLoTile + row) * rs + r) = w;
+                *reinterpret_cast<uint32_t*>(hs + (size_t)(u * kLoTile + row) * rs + r) = e;
             }
         }
         __syncthreads();
     }
-    const int c_end = min(a.N, (int)(blockIdx.y + 1) * a.cols);
-    for (int n0 = blockIdx.y * a.cols + 32 * warp; n0 < c_end; n0 += 32 * kLoWarps) {
-        const int col = n0 + 8 * q;  // this lane's 8 columns (N is a multiple of 8)
-        const bool cin = col < a.N;
-        // base first: its loads are under way while the products run
-        uint4 bv[4][kO16 ? 1 : 2];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int v = 0; v < (kO16 ? 1 : 2); ++v) {
-                bv[i][v] = make_uint4(0u, 0u, 0u, 0u);
-                if (a.base && cin && g + 8 * i < s.count)
-                    bv[i][v] = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.base) +
-                                                               ((size_t)s.token[g + 8 * i] * a.N + col) * (kO16 ? 2 : 4) + 16 * v);
-            }
+    for (; n0 < c_end;) {
         float acc[2][4][4];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
@@ -381,68 +451,74 @@ __global__ void __launch_bounds__(kLoThreads) lo_expand_kernel(const __grid_cons
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) acc[m][j][c] = 0.f;
-        // column g of MMA j is output column n0 + 8 (g / 2) + 2 j + g % 2: lane q's results are 8 q + 0..7
-        const int brow = n0 + 8 * (g >> 1) + (g & 1);
-        for (int r = 0; r < rank; r += 32) {
-            uint4 w[4];
+        for (int r = 0; r < rank; r += 64) {
+            if (r > 0) load_b(n0, r);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                w[j] = make_uint4(0u, 0u, 0u, 0u);
-                const int rr = r + 8 * q;
-                if (brow + 2 * j < a.N && rr < rank) {
-                    w[j] = *reinterpret_cast<const uint4*>(a.b + ((size_t)ad * a.N + brow + 2 * j) * a.R + rr);
-                    if (rr + 8 > rank) {  // what lies behind the adapter's rank does not count, whatever it is
-                        uint32_t* e = reinterpret_cast<uint32_t*>(&w[j]);
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            e[c] = rr + 2 * c + 1 < rank ? e[c] : rr + 2 * c < rank ? e[c] & 0xFFFFu : 0u;
-                    }
-                }
-            }
-#pragma unroll
-            for (int u = kParts - 1; u >= 0; --u) {
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    if (m == 1 && !two) break;
-                    const uint4 lo = *reinterpret_cast<const uint4*>(hs + (size_t)(u * kLoTile + 16 * m + g) * rs + r + 8 * q);
-                    const uint4 hi = *reinterpret_cast<const uint4*>(hs + (size_t)(u * kLoTile + 16 * m + g + 8) * rs + r + 8 * q);
+            for (int h = 0; h < 2; ++h) {
+                const int rr = r + 32 * h;
+                if (rr >= rank) break;
+                if (rr + 32 > rank) {  // what lies behind the adapter's rank does not count, whatever it is
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        mma_bf16(acc[m][j], lo.x, hi.x, lo.y, hi.y, w[j].x, w[j].y);
-                        mma_bf16(acc[m][j], lo.z, hi.z, lo.w, hi.w, w[j].z, w[j].w);
+                        uint32_t* e = reinterpret_cast<uint32_t*>(&w[h][j]);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const int at = rr + 8 * q + 2 * c;
+                            e[c] = at + 1 < rank ? e[c] : at < rank ? e[c] & 0xFFFFu : 0u;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int u = kParts - 1; u >= 0; --u) {
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        if (m == 1 && !two) break;
+                        const uint16_t* hp = hs + (size_t)(u * kLoTile + row0 + 16 * m) * rs + rr + 8 * q;
+                        const uint4 lo = *reinterpret_cast<const uint4*>(hp), hi = *reinterpret_cast<const uint4*>(hp + 8 * rs);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            mma_bf16(acc[m][j], lo.x, hi.x, lo.y, hi.y, w[h][j].x, w[h][j].y);
+                            mma_bf16(acc[m][j], lo.z, hi.z, lo.w, hi.w, w[h][j].z, w[h][j].w);
+                        }
                     }
                 }
             }
         }
+        const int col = n0 + 8 * q;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if (!cin || g + 8 * i >= s.count) continue;
+            if (col >= a.N || g + 8 * i >= left) continue;
             float o[8];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 o[2 * j] = acc[i >> 1][j][(i & 1) * 2];
                 o[2 * j + 1] = acc[i >> 1][j][(i & 1) * 2 + 1];
             }
-            char* dst = static_cast<char*>(a.out) + ((size_t)s.token[g + 8 * i] * a.N + col) * (kO16 ? 2 : 4);
+            char* dst = static_cast<char*>(a.out) + ((size_t)s.token[row0 + 8 * i] * a.N + col) * (kO16 ? 2 : 4);
             if constexpr (kO16) {
                 const uint32_t bw[4] = {bv[i][0].x, bv[i][0].y, bv[i][0].z, bv[i][0].w};
-                uint32_t w[4];
+                uint32_t e[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const __nv_bfloat162 v = __floats2bfloat162_rn(o[2 * c] + __uint_as_float(bw[c] << 16),
                                                                    o[2 * c + 1] + __uint_as_float(bw[c] & 0xFFFF0000u));
-                    w[c] = *reinterpret_cast<const uint32_t*>(&v);
+                    e[c] = *reinterpret_cast<const uint32_t*>(&v);
                 }
-                *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+                *reinterpret_cast<uint4*>(dst) = make_uint4(e[0], e[1], e[2], e[3]);
             } else {
                 const uint32_t bw[8] = {bv[i][0].x, bv[i][0].y, bv[i][0].z, bv[i][0].w,
-                                        bv[i][1].x, bv[i][1].y, bv[i][1].z, bv[i][1].w};
-                float r[8];
+                                        bv[i][kV - 1].x, bv[i][kV - 1].y, bv[i][kV - 1].z, bv[i][kV - 1].w};
+                float e[8];
 #pragma unroll
-                for (int c = 0; c < 8; ++c) r[c] = o[c] + __uint_as_float(bw[c]);
-                reinterpret_cast<float4*>(dst)[0] = make_float4(r[0], r[1], r[2], r[3]);
-                reinterpret_cast<float4*>(dst)[1] = make_float4(r[4], r[5], r[6], r[7]);
+                for (int c = 0; c < 8; ++c) e[c] = o[c] + __uint_as_float(bw[c]);
+                reinterpret_cast<float4*>(dst)[0] = make_float4(e[0], e[1], e[2], e[3]);
+                reinterpret_cast<float4*>(dst)[1] = make_float4(e[4], e[5], e[6], e[7]);
             }
+        }
+        n0 += 32 * nw;
+        if (n0 < c_end) {
+            load_base(n0);
+            load_b(n0, 0);
         }
     }
 }

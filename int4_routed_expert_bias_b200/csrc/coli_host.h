@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -49,9 +50,11 @@ inline bool overlap(const void* a, size_t na, const void* b, size_t nb)
 inline bool known_dtype(coli_dtype t) { return t == COLI_F32 || t == COLI_BF16; }
 inline size_t dtype_size(coli_dtype t) { return t == COLI_BF16 ? 2 : 4; }
 
-// Launch as a programmatic dependent of the previous kernel on the stream: its
-// launch may overlap the predecessor's tail; the kernel calls griddep_wait()
-// before it reads anything the predecessor wrote.
+// Launch as a programmatic dependent of the previous kernel on the stream,
+// whoever launched that one: its launch may overlap the predecessor's tail.  The
+// kernel's every thread calls griddep_wait() before it reads or writes anything
+// that an earlier kernel may touch (so when it is done, all before it is done), and
+// lets its own dependents start only after that.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, int block, size_t smem, cudaStream_t s, Args... args)
 {
@@ -66,6 +69,22 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, int block, size_t smem
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+// Allows a kernel its dynamic shared memory, once per device.
+template <auto kKernel>
+coli_status allow_smem_once(int bytes)
+{
+    static std::atomic<bool> done[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    if (dev < 0 || dev >= 64) return fail(COLI_ERR_UNSUPPORTED, "device %d out of range", dev);
+    if (done[dev].load(std::memory_order_acquire)) return COLI_OK;
+    if ((e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess)
+        return cuda_fail(e, "kernel attribute setup");
+    done[dev].store(true, std::memory_order_release);
+    return COLI_OK;
 }
 
 }  // namespace coli

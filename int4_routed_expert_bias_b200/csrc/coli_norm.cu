@@ -13,19 +13,17 @@ cudaError_t launch(const NormArgs& a, cudaStream_t s)
 {
     // Rows that are whole 16-byte vectors in every type (the pointers are 16-byte aligned) are read so;
     // other widths value by value.
+    auto go = [&](auto kern, int blocks, int threads) { return launch_pdl(kern, dim3(blocks), threads, 0, s, a); };
+    const int eighth = (a.T + 7) / 8;  // warp form: eight rows per block
     if (a.H % 8 == 0) {
         const int nv = a.H / 8;
-        if (nv <= 32) residual_norm_kernel<kD, kR, 8, 1, true><<<(a.T + 7) / 8, 256, 0, s>>>(a);
-        else if (nv <= 64) residual_norm_kernel<kD, kR, 8, 2, true><<<(a.T + 7) / 8, 256, 0, s>>>(a);
-        else residual_norm_kernel<kD, kR, 8, 2, false><<<a.T, ((nv + 1) / 2 + 31) / 32 * 32, 0, s>>>(a);
-    } else if (a.H <= 128) {
-        residual_norm_kernel<kD, kR, 1, 4, true><<<(a.T + 7) / 8, 256, 0, s>>>(a);
-    } else if (a.H <= 4096) {
-        residual_norm_kernel<kD, kR, 1, 4, false><<<a.T, ((a.H + 3) / 4 + 31) / 32 * 32, 0, s>>>(a);
-    } else {
-        residual_norm_kernel<kD, kR, 1, 16, false><<<a.T, 1024, 0, s>>>(a);
+        if (nv <= 32) return go(residual_norm_kernel<kD, kR, 8, 1, true>, eighth, 256);
+        if (nv <= 64) return go(residual_norm_kernel<kD, kR, 8, 2, true>, eighth, 256);
+        return go(residual_norm_kernel<kD, kR, 8, 2, false>, a.T, ((nv + 1) / 2 + 31) / 32 * 32);
     }
-    return cudaGetLastError();
+    if (a.H <= 128) return go(residual_norm_kernel<kD, kR, 1, 4, true>, eighth, 256);
+    if (a.H <= 4096) return go(residual_norm_kernel<kD, kR, 1, 4, false>, a.T, ((a.H + 3) / 4 + 31) / 32 * 32);
+    return go(residual_norm_kernel<kD, kR, 1, 16, false>, a.T, 1024);
 }
 
 coli_status check_norm(const coli_block_norm* n)

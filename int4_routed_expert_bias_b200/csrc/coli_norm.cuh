@@ -92,6 +92,7 @@ __global__ void __launch_bounds__(kWarpRow ? 256 : 1024) residual_norm_kernel(co
     __shared__ float red[2][32];
     const int lane = kWarpRow ? threadIdx.x & 31 : threadIdx.x, width = kWarpRow ? 32 : blockDim.x;
     const int t = kWarpRow ? blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+    griddep_wait();
     if (t >= a.T) return;  // whole warps (or none) leave
     const size_t row = (size_t)t * a.H;
     float d[kN][kVec], r[kN][kVec];

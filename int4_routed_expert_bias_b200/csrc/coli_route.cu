@@ -1,7 +1,6 @@
 // coli_route.cu -- host side of the general router (coli_router_forward).
 #include <algorithm>
 #include <cmath>
-#include <mutex>
 
 #include "coli_host.h"
 #include "coli_route.cuh"
@@ -90,34 +89,13 @@ template <bool kBf16>
 cudaError_t launch_rows(const RouteArgs& a, int mt, cudaStream_t s)
 {
     const dim3 grid((a.E * a.splits + kRouteWarps - 1) / kRouteWarps, (a.T + mt - 1) / mt);
+    auto go = [&](auto kern) { return launch_pdl(kern, grid, kRouteThreads, 0, s, a); };
     switch (mt) {
-        case 1: route_rows_kernel<1, kBf16><<<grid, kRouteThreads, 0, s>>>(a); break;
-        case 2: route_rows_kernel<2, kBf16><<<grid, kRouteThreads, 0, s>>>(a); break;
-        case 4: route_rows_kernel<4, kBf16><<<grid, kRouteThreads, 0, s>>>(a); break;
-        default: route_rows_kernel<8, kBf16><<<grid, kRouteThreads, 0, s>>>(a); break;
+        case 1: return go(route_rows_kernel<1, kBf16>);
+        case 2: return go(route_rows_kernel<2, kBf16>);
+        case 4: return go(route_rows_kernel<4, kBf16>);
+        default: return go(route_rows_kernel<8, kBf16>);
     }
-    return cudaGetLastError();
-}
-
-// The batch kernel's shared memory is allowed once per device.
-std::mutex g_allow_mu;
-bool g_allowed[64];
-
-coli_status allow_batch_kernels()
-{
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-    if (dev < 0 || dev >= 64) return fail(COLI_ERR_UNSUPPORTED, "device %d out of range", dev);
-    std::lock_guard<std::mutex> lock(g_allow_mu);
-    if (g_allowed[dev]) return COLI_OK;
-    if ((e = cudaFuncSetAttribute(route_gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  (int)RgShape<true>::kSmem)) != cudaSuccess ||
-        (e = cudaFuncSetAttribute(route_gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  (int)RgShape<false>::kSmem)) != cudaSuccess)
-        return cuda_fail(e, "kernel attribute setup");
-    g_allowed[dev] = true;
-    return COLI_OK;
 }
 
 template <bool kBf16>
@@ -127,9 +105,8 @@ cudaError_t launch_batch(const RouteArgs& a, const RoutePlan& p, cudaStream_t s)
     if (kBf16 && !encode_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.x, (uint64_t)a.H, (uint64_t)a.T, kRgK, kRgM,
                             CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
-    route_gemm_kernel<kBf16><<<dim3(p.m_tiles, p.e_tiles, p.splits), kRgThreads, RgShape<kBf16>::kSmem, s>>>(
-        tx, a, p.ET, wait_limit(kRgWaitNs));
-    return cudaGetLastError();
+    return launch_pdl(route_gemm_kernel<kBf16>, dim3(p.m_tiles, p.e_tiles, p.splits), kRgThreads, RgShape<kBf16>::kSmem, s,
+                      tx, a, p.ET, wait_limit(kRgWaitNs));
 }
 
 template <bool kBf16>
@@ -200,7 +177,9 @@ coli_status coli_router_forward(const coli_router* r, const void* x, coli_dtype 
     if (p.batch) {
         if (bf16 && !tensor_map_encoder())
             return fail(COLI_ERR_UNSUPPORTED, "the CUDA driver provides no cuTensorMapEncodeTiled (tensor-core router path)");
-        if ((st = allow_batch_kernels()) != COLI_OK) return st;
+        st = bf16 ? allow_smem_once<route_gemm_kernel<true>>((int)RgShape<true>::kSmem)
+                  : allow_smem_once<route_gemm_kernel<false>>((int)RgShape<false>::kSmem);
+        if (st != COLI_OK) return st;
         e = bf16 ? launch_batch<true>(a, p, stream) : launch_batch<false>(a, p, stream);
     } else {
         e = bf16 ? launch_rows<true>(a, p.mt, stream) : launch_rows<false>(a, p.mt, stream);

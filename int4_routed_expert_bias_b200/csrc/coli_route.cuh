@@ -60,6 +60,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_rows_kernel(const __grid_
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int unit = blockIdx.x * kRouteWarps + warp;
+    griddep_wait();
     griddep_launch_dependents();
     if (unit >= a.E * a.splits) return;
     const int e = unit / a.splits, sp = unit - e * a.splits;
@@ -212,6 +213,7 @@ route_gemm_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant_
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base;
+    griddep_wait();
     const unsigned long long deadline = global_ns() + wait_ns;
 
     if (warp < kRgWarpEpi) {
