@@ -667,97 +667,179 @@ struct GroupState {
     uint32_t kept;      // bit per group
 };
 
-// The selection of one token with a few open decisions, by one warp: the border
-// groups' leading experts are summed in double and the border drawn again; then
-// the ranking in fp32 is carried on past k until a clear gap, and every run of
-// neighbours without a clear gap is ordered by double sums.  Lane j < k returns
-// slot j.  false: too many open decisions, or the softmax denominator's own
-// error matters (route_exact takes those).
+// Dot products in double that one warp of a block asks for and all of its warps
+// compute: each takes every eighth 128 values of the row, and the eight parts are
+// added in order, so equal rows of W stay equal.
+struct RouteDots {
+    int n;
+    int e[32];
+    double part[kRouteWarps][32];
+    __device__ __forceinline__ double z(int i) const
+    {
+        double s = 0.;
+#pragma unroll
+        for (int w = 0; w < kRouteWarps; ++w) s += part[w][i];
+        return s;
+    }
+};
+
+// The whole block calls it; d.n and d.e were written by one warp before.
+__device__ __forceinline__ void block_dots(const RouteArgs& a, bool bf16, int t, RouteDots& d)
+{
+    __syncthreads();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = d.n;
+    const char* xr = static_cast<const char*>(a.x) + (size_t)t * a.H * (bf16 ? 2 : 4);
+    for (int b = 0; b < n; b += 4) {
+        const float* w[4];
+        double z[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            w[j] = a.w_router + (size_t)d.e[min(b + j, n - 1)] * a.H;
+            z[j] = 0.;
+        }
+#pragma unroll 2
+        for (int i = 128 * warp + 4 * lane; i < a.H; i += 128 * kRouteWarps) {
+            const float4 v = bf16 ? load_act4<true>(xr, i) : load_act4<false>(xr, i);
+            float4 u[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) u[j] = *reinterpret_cast<const float4*>(w[j] + i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                z[j] = fma((double)u[j].x, (double)v.x, z[j]);
+                z[j] = fma((double)u[j].y, (double)v.y, z[j]);
+                z[j] = fma((double)u[j].z, (double)v.z, z[j]);
+                z[j] = fma((double)u[j].w, (double)v.w, z[j]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) z[j] = warp_sum_d(z[j]);
+        if (lane < 4 && b + lane < n) d.part[warp][b + lane] = lane == 0 ? z[0] : lane == 1 ? z[1] : lane == 2 ? z[2] : z[3];
+    }
+    __syncthreads();
+}
+
+// The selection of one token with a few open decisions.  The block calls it; the
+// warp with `owner` decides, all of them sum.  The border groups' leading experts
+// are summed in double and the border drawn again; then the ranking in fp32 is
+// carried on past k until a clear gap, and every run of neighbours without a clear
+// gap is ordered by double sums.  Lane j < k of the owner returns slot j; false:
+// too many open decisions, or the softmax denominator's own error matters
+// (route_exact takes those).
 __device__ __noinline__ bool route_close(const RouteArgs& a, bool bf16, int t, const float* z_s, const float* c_s, float dz,
-                                         float zm, float den, GroupState gs, int& my_e, double& my_p)
+                                         float zm, float den, GroupState gs, bool owner, RouteDots& d, int& my_e, double& my_p)
 {
     const int lane = threadIdx.x & 31;
     const unsigned full = 0xFFFFFFFFu;
     const int E = a.E, G = a.groups, m = E / G;
     const double dd = a.softmax && a.bias ? (double)dz + 0x1p-20 : 0.;  // relative error of the denominator
-    auto at = [&](int e) { return G > 1 ? e + (int)(e * a.gmul >> 20) : e; };
-    if (G > 1 && gs.lo - gs.hi <= 2.f * gs.err) {
-        const bool in = lane < G && ((gs.kept >> lane) & 1u);
-        const bool open = lane < G && (in ? gs.score - gs.hi <= 2.f * gs.err : gs.lo - gs.score <= 2.f * gs.err);
-        const uint32_t border = __ballot_sync(full, open);
-        double sc = 0., sp = 0.;  // lane g: the score of a border group, and its part without biases
-        for (uint32_t left = border; left; left &= left - 1) {
-            const int g = __ffs(left) - 1;
-            const float floor_c = __shfl_sync(full, gs.last, g) - 2.f * gs.err;
-            double v1 = -INFINITY, v2 = -INFINITY, p1 = 0., p2 = 0.;
-            for (int b = g * m; b < (g + 1) * m; b += 32) {
-                const uint32_t cand = __ballot_sync(full, b + lane < (g + 1) * m && c_s[at(b + lane)] >= floor_c);
-                route_dots(
-                    a, bf16, t, cand, [&](int i) { return b + i; },
-                    [&](int, int e, double z) {
-                        double p;
-                        const double v = choice_exact(a, e, z, zm, den, p);
-                        if (v > v1) v2 = v1, p2 = p1, v1 = v, p1 = p;
-                        else if (v > v2) v2 = v, p2 = p;
-                    });
+    auto group_of = [&](int e) { return (int)(e * a.gmul >> 20); };
+    auto at = [&](int e) { return G > 1 ? e + group_of(e) : e; };
+    bool ok = true;
+
+    // the border between kept and rejected groups
+    const bool border_open = G > 1 && gs.lo - gs.hi <= 2.f * gs.err;
+    bool open = false;
+    uint32_t border = 0;
+    if (owner) {
+        int n = 0;
+        if (border_open) {
+            const bool in = lane < G && ((gs.kept >> lane) & 1u);
+            open = lane < G && (in ? gs.score - gs.hi <= 2.f * gs.err : gs.lo - gs.score <= 2.f * gs.err);
+            border = __ballot_sync(full, open);
+            for (uint32_t left = border; left; left &= left - 1) {
+                const int g = __ffs(left) - 1;
+                const float floor_c = __shfl_sync(full, gs.last, g) - 2.f * gs.err;
+                for (int b = g * m; b < (g + 1) * m; b += 32) {
+                    const bool mine = b + lane < (g + 1) * m && c_s[at(b + lane)] >= floor_c;
+                    const uint32_t cand = __ballot_sync(full, mine);
+                    const int pos = n + __popc(cand & ((1u << lane) - 1u));
+                    if (mine && pos < 32) d.e[pos] = b + lane;
+                    n += __popc(cand);
+                }
             }
-            if (lane == g) sc = a.top == 2 ? v1 + v2 : v1, sp = a.top == 2 ? p1 + p2 : p1;
         }
-        const int slots = a.keep - __popc(gs.kept & ~border);
-        int rank = 0;
-        for (uint32_t left = border; left; left &= left - 1) {
-            const int g = __ffs(left) - 1;
-            const double o = __shfl_sync(full, sc, g);
-            rank += (o > sc || (o == sc && g < lane)) ? 1 : 0;
-        }
-        const uint32_t chosen = __ballot_sync(full, open && rank < slots);
-        bool close = false;
-        for (uint32_t left = border; left; left &= left - 1) {
-            const int g = __ffs(left) - 1;
-            const double o = __shfl_sync(full, sc, g), op = __shfl_sync(full, sp, g);
-            close |= open && ((chosen >> g) & 1u) != ((chosen >> lane) & 1u) && fabs(o - sc) < dd * fabs(op - sp);
-        }
-        if (__any_sync(full, close)) return false;
-        gs.kept = (gs.kept & ~border) | chosen;
+        if (n > 32) ok = false, n = 0;
+        if (lane == 0) d.n = n;
     }
+    block_dots(a, bf16, t, d);
+    if (owner) {
+        if (border_open && ok) {
+            double v1 = -INFINITY, v2 = -INFINITY, p1 = 0., p2 = 0.;  // lane g: its group's best
+            for (int i = 0; i < d.n; ++i) {
+                const int e = d.e[i];
+                double p;
+                const double v = choice_exact(a, e, d.z(i), zm, den, p);
+                if (lane == group_of(e)) {
+                    if (v > v1) v2 = v1, p2 = p1, v1 = v, p1 = p;
+                    else if (v > v2) v2 = v, p2 = p;
+                }
+            }
+            const double sc = a.top == 2 ? v1 + v2 : v1, sp = a.top == 2 ? p1 + p2 : p1;
+            const int slots = a.keep - __popc(gs.kept & ~border);
+            int rank = 0;
+            for (uint32_t left = border; left; left &= left - 1) {
+                const int g = __ffs(left) - 1;
+                const double o = __shfl_sync(full, sc, g);
+                rank += (o > sc || (o == sc && g < lane)) ? 1 : 0;
+            }
+            const uint32_t chosen = __ballot_sync(full, open && rank < slots);
+            bool close = false;
+            for (uint32_t left = border; left; left &= left - 1) {
+                const int g = __ffs(left) - 1;
+                const double o = __shfl_sync(full, sc, g), op = __shfl_sync(full, sp, g);
+                close |= open && ((chosen >> g) & 1u) != ((chosen >> lane) & 1u) && fabs(o - sc) < dd * fabs(op - sp);
+            }
+            if (__any_sync(full, close)) ok = false;
+            gs.kept = (gs.kept & ~border) | chosen;
+        }
+        __syncwarp();
+    }
+
     // fp32 ranking until a clear gap behind slot k
-    float my_c = 0.f, my_u = 0.f, prev_c = INFINITY;
-    int prev_e = -1, n = 0;
-    my_e = 0;
-    const int most = min(32, G > 1 ? a.keep * m : E);
-    for (; n < most; ++n) {
-        float bc = -INFINITY;
-        int be = 1 << 20;
-        for (int e = lane; e < E; e += 32) {
-            if (G > 1 && !((gs.kept >> (e * a.gmul >> 20)) & 1u)) continue;
-            const float c = c_s[at(e)];
-            if (!(c < prev_c || (c == prev_c && e > prev_e))) continue;  // taken
-            if (be == 1 << 20 || c > bc) bc = c, be = e;
+    float my_c = 0.f, my_u = 0.f;
+    int n = 0;
+    uint32_t runs = 0;     // lane j and j + 1 without a clear gap
+    uint32_t involved = 0;
+    if (owner) {
+        my_e = 0;
+        float prev_c = INFINITY;
+        int prev_e = -1;
+        const int all = G > 1 ? a.keep * m : E, most = ok ? min(32, all) : 0;
+        for (; n < most; ++n) {
+            float bc = -INFINITY;
+            int be = 1 << 20;
+            for (int e = lane; e < E; e += 32) {
+                if (G > 1 && !((gs.kept >> group_of(e)) & 1u)) continue;
+                const float c = c_s[at(e)];
+                if (!(c < prev_c || (c == prev_c && e > prev_e))) continue;  // taken
+                if (be == 1 << 20 || c > bc) bc = c, be = e;
+            }
+            const uint32_t key = be == 1 << 20 ? 0u : order_key(bc);
+            const uint32_t top = __reduce_max_sync(full, key);
+            const int e = (int)__reduce_min_sync(full, key == top ? (uint32_t)be : 0xFFFFFFFFu);
+            const float c = order_value(top);
+            const float s = a.softmax ? expf(z_s[e] - zm) / den : 1.0f / (1.0f + expf(-z_s[e]));
+            const float u = choice_err(a.softmax, s, c, dz);
+            if (lane == n) my_e = e, my_c = c, my_u = u, my_p = (double)s;
+            const float last_u = __shfl_sync(full, my_u, n > 0 ? n - 1 : 0);
+            if (n >= a.k && !(prev_c - c <= last_u + u)) break;  // slot k is clear of everything behind
+            prev_c = c, prev_e = e;
         }
-        const uint32_t key = be == 1 << 20 ? 0u : order_key(bc);
-        const uint32_t top = __reduce_max_sync(full, key);
-        const int e = (int)__reduce_min_sync(full, key == top ? (uint32_t)be : 0xFFFFFFFFu);
-        const float c = order_value(top);
-        const float s = a.softmax ? expf(z_s[e] - zm) / den : 1.0f / (1.0f + expf(-z_s[e]));
-        const float u = choice_err(a.softmax, s, c, dz);
-        if (lane == n) my_e = e, my_c = c, my_u = u, my_p = (double)s;
-        const float last_u = __shfl_sync(full, my_u, n > 0 ? n - 1 : 0);
-        if (n >= a.k && !(prev_c - c <= last_u + u)) break;  // slot k is clear of everything behind
-        prev_c = c, prev_e = e;
+        if (n == 32 && n < all) ok = false, n = 0;
+        const float nc = __shfl_down_sync(full, my_c, 1), nu = __shfl_down_sync(full, my_u, 1);
+        runs = __ballot_sync(full, lane + 1 < n && my_c - nc <= my_u + nu);
+        involved = runs | (runs << 1);
+        if ((involved >> lane) & 1u) d.e[__popc(involved & ((1u << lane) - 1u))] = my_e;
+        if (lane == 0) d.n = __popc(involved);
     }
-    if (n == 32 && n < (G > 1 ? a.keep * m : E)) return false;
-    const float nc = __shfl_down_sync(full, my_c, 1), nu = __shfl_down_sync(full, my_u, 1);
-    const uint32_t open = __ballot_sync(full, lane + 1 < n && my_c - nc <= my_u + nu);
+    block_dots(a, bf16, t, d);
+    if (!owner || !ok) return ok;
     double v = (double)my_c;
-    route_dots(
-        a, bf16, t, open | (open << 1), [&](int j) { return __shfl_sync(full, my_e, j); },
-        [&](int j, int e, double z) {
-            double p;
-            const double w = choice_exact(a, e, z, zm, den, p);
-            if (lane == j) v = w, my_p = p;
-        });
+    if ((involved >> lane) & 1u)
+        v = choice_exact(a, my_e, d.z(__popc(involved & ((1u << lane) - 1u))), zm, den, my_p);
+    __syncwarp();
     // slot of each: runs stay in place, inside a run by the double sums (equal: lower expert first)
-    const int run = __popc(~open & ((1u << lane) - 1u));
+    const int run = __popc(~runs & ((1u << lane) - 1u));
     int slot = 0;
     bool close = false;
     for (int i = 0; i < n; ++i) {
@@ -794,7 +876,7 @@ __host__ __device__ __forceinline__ size_t route_token_smem(int E)
 // token selects.  kPer = experts per lane.  Latency-bound: k + 1 rounds of a
 // warp-wide maximum (one redux instruction) over order-preserving integer keys.
 template <int kPer, bool kBf16>
-__global__ void __launch_bounds__(kRouteThreads, kPer <= 8 ? 3 : 2) route_select_kernel(const __grid_constant__ RouteArgs a, int tokens)
+__global__ void __launch_bounds__(kRouteThreads, 2) route_select_kernel(const __grid_constant__ RouteArgs a, int tokens)
 {
     extern __shared__ __align__(16) unsigned char route_smem[];
     const unsigned full = 0xFFFFFFFFu;
@@ -812,177 +894,207 @@ __global__ void __launch_bounds__(kRouteThreads, kPer <= 8 ? 3 : 2) route_select
         if (lane == 0) *a.status = bad;
     }
     {
-        const int Eq = a.Ep / 4;
+        // The token's share of the threads: `sets` times its Eq quads of experts, each set
+        // taking every sets-th partial; the sets are added in order.
+        const int Eq = a.Ep / 4, nthr = kRouteThreads / tokens, sub = threadIdx.x / nthr, u = threadIdx.x - sub * nthr;
+        const int sets = max(1, min(min(4, a.splits), nthr / Eq));
+        const int set = u / Eq;
         const size_t plane = (size_t)a.T * a.Ep;
-        const int per = kRouteWarps / tokens;  // warps per token (tokens is a power of two)
-        const int wt = warp / per;
-        if (wt < nt) {
-            float* dst = reinterpret_cast<float*>(route_smem + wt * stride);
-            const float* row = a.part + (size_t)(t0 + wt) * a.Ep;
-            for (int q = (warp - wt * per) * 32 + lane; q < Eq; q += per * 32) {
+        float* dst = reinterpret_cast<float*>(route_smem + sub * stride);
+        float4* side = reinterpret_cast<float4*>(route_smem + sub * stride + align_up((size_t)E * 4, 16));  // [sets][Eq]
+        if (sub < nt && (sets == 1 || set < sets)) {
+            const float* row = a.part + (size_t)(t0 + sub) * a.Ep;
+            for (int q = sets == 1 ? u : u - set * Eq; q < Eq; q += sets == 1 ? nthr : Eq) {
                 const float* p = row + 4 * q;
-                float4 v = *reinterpret_cast<const float4*>(p);
-                for (int s0 = 1; s0 < a.splits; s0 += 8) {  // up to eight independent loads at a time
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int s0 = sets == 1 ? 0 : set; s0 < a.splits; s0 += 8 * sets) {  // up to eight independent loads at a time
                     float4 o[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        if (s0 + j < a.splits) o[j] = *reinterpret_cast<const float4*>(p + (s0 + j) * plane);
+                        if (s0 + j * sets < a.splits) o[j] = *reinterpret_cast<const float4*>(p + (s0 + j * sets) * plane);
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        if (s0 + j < a.splits) v.x += o[j].x, v.y += o[j].y, v.z += o[j].z, v.w += o[j].w;
+                        if (s0 + j * sets < a.splits) v.x += o[j].x, v.y += o[j].y, v.z += o[j].z, v.w += o[j].w;
                 }
-                *reinterpret_cast<float4*>(dst + 4 * q) = v;  // the row's padding has room
+                if (sets == 1) *reinterpret_cast<float4*>(dst + 4 * q) = v;  // the row's padding has room
+                else side[set * Eq + q] = v;
+            }
+        }
+        if (sets > 1) {
+            __syncthreads();
+            for (int q = u; sub < nt && q < Eq; q += nthr) {
+                float4 v = side[q];
+                for (int i = 1; i < sets; ++i) {
+                    const float4 o = side[i * Eq + q];
+                    v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+                }
+                *reinterpret_cast<float4*>(dst + 4 * q) = v;
             }
         }
     }
     __syncthreads();
-    if (warp >= nt) return;
-    const int t = t0 + warp;
-    unsigned char* base = route_smem + warp * stride;
+    const bool has_token = warp < nt;
+    const int t = t0 + (has_token ? warp : 0);
+    unsigned char* base = route_smem + (has_token ? warp : 0) * stride;
     const float* z_s = reinterpret_cast<const float*>(base);
     double* zd = reinterpret_cast<double*>(base + align_up((size_t)E * 4, 16));
     double* pd = zd + align_up((size_t)E * 8, 16) / 8;
     float* c_s = reinterpret_cast<float*>(pd);
     unsigned char* st = base + stride - align_up((size_t)E, 16);
 
-    float c[kPer];
-    float zmax = 0.f, zm = -INFINITY;
-    bool odd = false;  // a score that is not finite
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int e = lane + 32 * i;
-        c[i] = e < E ? z_s[e] : 0.f;
-        zmax = fmaxf(zmax, fabsf(c[i]));
-        odd |= !(fabsf(c[i]) < INFINITY);
-        if (e < E) zm = fmaxf(zm, c[i]);
-    }
-    zmax = warp_max(zmax);
-    const float dz = a.sum_err * zmax;
-    // s_e: the unbiased score
-    float den = 1.f;
-    if (a.softmax) {
-        zm = warp_max(zm);
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            c[i] = lane + 32 * i < E ? expf(c[i] - zm) : 0.f;
-            sum += c[i];
-        }
-        den = warp_sum(sum);
-    }
-    auto score_of = [&](float v) { return a.softmax ? expf(v - zm) / den : 1.0f / (1.0f + expf(-v)); };
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const float s = a.softmax ? c[i] / den : 1.0f / (1.0f + expf(-c[i]));
-        const float v = s + bias[i];
-        c[i] = v == v ? v : -INFINITY;  // NaN ranks last: the order stays total
-    }
-
-    // eligible groups
-    uint32_t kept = full;  // bit per group
+    // what close decisions need of the usual path
+    float dz = 0.f, zm = -INFINITY, den = 1.f, my_s = 0.f;
+    int my_e = 0;
     bool open = false;
-    const int G = a.groups, m = E / G;
     GroupState gs{0.f, 0.f, 0.f, 0.f, 0.f, full};
-    if (G > 1) {
+    if (has_token) {
+        float c[kPer];
+        float zmax = 0.f;
+        bool odd = false;  // a score that is not finite
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int e = lane + 32 * i;
-            if (e < E) c_s[e + (int)(e * a.gmul >> 20)] = c[i];
+            c[i] = e < E ? z_s[e] : 0.f;
+            zmax = fmaxf(zmax, fabsf(c[i]));
+            odd |= !(fabsf(c[i]) < INFINITY);
+            if (e < E) zm = fmaxf(zm, c[i]);
         }
-        __syncwarp();
-        // 2^floor(log2(32 / G)) lanes per group, each a strided share of its experts
-        const int lsh = 31 - __clz(32 / G), lg = 1 << lsh;
-        const int g = lane >> lsh, r = lane & (lg - 1);
-        float b1 = -INFINITY, b2 = -INFINITY;
-        if (g < G) {
-            for (int j = r; j < m; j += lg) {
-                const float v = c_s[g * (m + 1) + j];
-                b2 = fmaxf(b2, fminf(b1, v));
-                b1 = fmaxf(b1, v);
+        zmax = warp_max(zmax);
+        dz = a.sum_err * zmax;
+        // s_e: the unbiased score
+        if (a.softmax) {
+            zm = warp_max(zm);
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                c[i] = lane + 32 * i < E ? expf(c[i] - zm) : 0.f;
+                sum += c[i];
             }
+            den = warp_sum(sum);
         }
-        for (int o = lg >> 1; o > 0; o >>= 1) {
-            const float o1 = __shfl_xor_sync(full, b1, o), o2 = __shfl_xor_sync(full, b2, o);
-            b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
-            b1 = fmaxf(b1, o1);
+        auto score_of = [&](float v) { return a.softmax ? expf(v - zm) / den : 1.0f / (1.0f + expf(-v)); };
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const float s = a.softmax ? c[i] / den : 1.0f / (1.0f + expf(-c[i]));
+            const float v = s + bias[i];
+            c[i] = v == v ? v : -INFINITY;  // NaN ranks last: the order stays total
         }
-        const float s_most = a.softmax ? 1.f / den : 0.5f;
-        float err = choice_err(a.softmax, s_most, b1, dz);
-        float score = b1;
-        if (a.top == 2) {
-            err += choice_err(a.softmax, s_most, b2, dz);
-            score = b1 + b2;
-        }
-        if (!(score == score)) score = -INFINITY;
-        // lane g takes over group g
-        const int from = (lane << lsh) & 31;
-        gs.score = __shfl_sync(full, score, from);
-        gs.last = __shfl_sync(full, a.top == 2 ? b2 : b1, from);
-        int rank = 0;
-        for (int h = 0; h < G; ++h) {
-            const float o = __shfl_sync(full, gs.score, h);
-            rank += (o > gs.score || (o == gs.score && h < lane)) ? 1 : 0;
-        }
-        const bool in = lane < G && rank < a.keep;
-        kept = __ballot_sync(full, in);
-        gs.lo = warp_min(in ? gs.score : INFINITY);
-        gs.hi = warp_max(lane < G && !in ? gs.score : -INFINITY);
-        gs.err = warp_max(g < G ? err : 0.f);
-        gs.kept = kept;
-        open = gs.lo - gs.hi <= 2.f * gs.err;
-    }
 
-    uint32_t key[kPer];
+        // eligible groups
+        uint32_t kept = full;  // bit per group
+        const int G = a.groups, m = E / G;
+        if (G > 1) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int e = lane + 32 * i;
-        key[i] = e < E && (G == 1 || ((kept >> (e * a.gmul >> 20)) & 1u)) ? order_key(c[i]) : 0u;
-    }
-    // k rounds (and one more, for the gap to the first rejected expert)
-    int my_e = 0;
-    float my_c = 0.f, next_c = -INFINITY;
-    int next_e = -1;
-    const int rounds = a.k + (a.k < (G > 1 ? a.keep * m : E) ? 1 : 0);
-    for (int j = 0; j < rounds; ++j) {
-        uint32_t best = key[0];
-        int bi = 0;
-#pragma unroll
-        for (int i = 1; i < kPer; ++i)
-            if (key[i] > best) best = key[i], bi = i;
-        const uint32_t top = __reduce_max_sync(full, best);
-        const int e = (int)__reduce_min_sync(full, best == top ? (uint32_t)(lane + 32 * bi) : 0xFFFFFFFFu);
-        if (lane == (e & 31)) {
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                if (i == (e >> 5)) key[i] = 0u;
+            for (int i = 0; i < kPer; ++i) {
+                const int e = lane + 32 * i;
+                if (e < E) c_s[e + (int)(e * a.gmul >> 20)] = c[i];
+            }
+            __syncwarp();
+            // 2^floor(log2(32 / G)) lanes per group, each a strided share of its experts
+            const int lsh = 31 - __clz(32 / G), lg = 1 << lsh;
+            const int g = lane >> lsh, r = lane & (lg - 1);
+            float b1 = -INFINITY, b2 = -INFINITY;
+            if (g < G) {
+                for (int j = r; j < m; j += lg) {
+                    const float v = c_s[g * (m + 1) + j];
+                    b2 = fmaxf(b2, fminf(b1, v));
+                    b1 = fmaxf(b1, v);
+                }
+            }
+            for (int o = lg >> 1; o > 0; o >>= 1) {
+                const float o1 = __shfl_xor_sync(full, b1, o), o2 = __shfl_xor_sync(full, b2, o);
+                b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
+                b1 = fmaxf(b1, o1);
+            }
+            const float s_most = a.softmax ? 1.f / den : 0.5f;
+            float err = choice_err(a.softmax, s_most, b1, dz);
+            float score = b1;
+            if (a.top == 2) {
+                err += choice_err(a.softmax, s_most, b2, dz);
+                score = b1 + b2;
+            }
+            if (!(score == score)) score = -INFINITY;
+            // lane g takes over group g
+            const int from = (lane << lsh) & 31;
+            gs.score = __shfl_sync(full, score, from);
+            gs.last = __shfl_sync(full, a.top == 2 ? b2 : b1, from);
+            int rank = 0;
+            for (int h = 0; h < G; ++h) {
+                const float o = __shfl_sync(full, gs.score, h);
+                rank += (o > gs.score || (o == gs.score && h < lane)) ? 1 : 0;
+            }
+            const bool in = lane < G && rank < a.keep;
+            kept = __ballot_sync(full, in);
+            gs.lo = warp_min(in ? gs.score : INFINITY);
+            gs.hi = warp_max(lane < G && !in ? gs.score : -INFINITY);
+            gs.err = warp_max(g < G ? err : 0.f);
+            gs.kept = kept;
+            open = gs.lo - gs.hi <= 2.f * gs.err;
         }
-        const float v = order_value(top);
-        if (j == a.k) next_c = v, next_e = e;
-        else if (lane == j) my_e = e, my_c = v;
-    }
-    float my_s = score_of(z_s[my_e]);
-    {
-        // gaps between neighbours in rank against what the fp32 sums can carry
-        const float my_u = choice_err(a.softmax, my_s, my_c, dz);
-        float nc = __shfl_down_sync(full, my_c, 1), nu = __shfl_down_sync(full, my_u, 1);
-        bool has = lane + 1 < a.k;
-        if (lane == a.k - 1 && next_e >= 0) {
-            nc = next_c;
-            nu = choice_err(a.softmax, score_of(z_s[next_e]), next_c, dz);
-            has = true;
+
+        uint32_t key[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int e = lane + 32 * i;
+            key[i] = e < E && (G == 1 || ((kept >> (e * a.gmul >> 20)) & 1u)) ? order_key(c[i]) : 0u;
         }
-        open |= has && my_c - nc <= my_u + nu;
-    }
-    open = __any_sync(full, open) && !__any_sync(full, odd);
-    if (open) {
-        double p = 0.;
-        if (G == 1) {
+        // k rounds (and one more, for the gap to the first rejected expert)
+        float my_c = 0.f, next_c = -INFINITY;
+        int next_e = -1;
+        const int rounds = a.k + (a.k < (G > 1 ? a.keep * m : E) ? 1 : 0);
+        for (int j = 0; j < rounds; ++j) {
+            uint32_t best = key[0];
+            int bi = 0;
+#pragma unroll
+            for (int i = 1; i < kPer; ++i)
+                if (key[i] > best) best = key[i], bi = i;
+            const uint32_t top = __reduce_max_sync(full, best);
+            const int e = (int)__reduce_min_sync(full, best == top ? (uint32_t)(lane + 32 * bi) : 0xFFFFFFFFu);
+            if (lane == (e & 31)) {
+#pragma unroll
+                for (int i = 0; i < kPer; ++i)
+                    if (i == (e >> 5)) key[i] = 0u;
+            }
+            const float v = order_value(top);
+            if (j == a.k) next_c = v, next_e = e;
+            else if (lane == j) my_e = e, my_c = v;
+        }
+        my_s = score_of(z_s[my_e]);
+        {
+            // gaps between neighbours in rank against what the fp32 sums can carry
+            const float my_u = choice_err(a.softmax, my_s, my_c, dz);
+            float nc = __shfl_down_sync(full, my_c, 1), nu = __shfl_down_sync(full, my_u, 1);
+            bool has = lane + 1 < a.k;
+            if (lane == a.k - 1 && next_e >= 0) {
+                nc = next_c;
+                nu = choice_err(a.softmax, score_of(z_s[next_e]), next_c, dz);
+                has = true;
+            }
+            open |= has && my_c - nc <= my_u + nu;
+        }
+        open = __any_sync(full, open) && !__any_sync(full, odd);
+        if (open && G == 1) {
 #pragma unroll
             for (int i = 0; i < kPer; ++i)
                 if (lane + 32 * i < E) c_s[lane + 32 * i] = c[i];
         }
-        __syncwarp();
-        if (dz == 0.f || !route_close(a, kBf16, t, z_s, c_s, dz, zm, den, gs, my_e, p)) {
+    }
+    __shared__ unsigned char open_s[kRouteWarps];
+    __shared__ RouteDots dots;
+    if (lane == 0) open_s[warp] = open && dz != 0.f;
+    __syncthreads();
+    double p = 0.;
+    bool settled = false;
+    for (int o = 0; o < nt; ++o)
+        if (open_s[o]) {
+            const bool owner = warp == o;
+            const bool done = route_close(a, kBf16, t0 + o, z_s, c_s, dz, zm, den, gs, owner, dots, my_e, p);
+            if (owner) settled = done;
+            __syncthreads();
+        }
+    if (!has_token) return;
+    if (open) {
+        if (!settled) {  // (scores that are exact as they are, dz == 0, come here at once)
             __syncwarp();
             route_exact(a, kBf16, t, z_s, zd, pd, st, (double)dz, my_e, p);
         }
