@@ -424,7 +424,9 @@ COLI_API size_t coli_adapters_workspace_size(const coli_adapters* adapters, int 
  * relative); out is rounded once.  A non-finite activation makes its own row of
  * out non-finite (NaN where a sum would be infinite).  Deterministic.  Workspace as in
  * coli_router_forward (256-byte aligned, undefined on entry, not shared by calls
- * that may run concurrently).  T == 0 launches nothing.
+ * that may run concurrently; its first 4 bytes are the status word: 0, or 1 when a
+ * pipeline wait of the kernels for batches of more than 64 tokens ran out).
+ * T == 0 launches nothing.
  */
 COLI_API coli_status coli_adapters_forward(const coli_adapters* adapters, const void* x, coli_dtype xt, int T,
                                            const int32_t* which, const void* base, void* out, coli_dtype ot,

@@ -2,6 +2,7 @@
 #include <algorithm>
 
 #include "coli_adapters.cuh"
+#include "coli_adapters_tc.cuh"
 #include "coli_host.h"
 
 using namespace coli;
@@ -29,31 +30,45 @@ coli_status check_adapters(const coli_adapters* d, int T)
     return COLI_OK;
 }
 
+constexpr size_t kStatusBytes = 256;  // the status word and its padding, at the start of the workspace
+
 struct LoPlan {
     int max_tiles, pieces, chunk, cols;
-    size_t perm, tiles, n_tiles, bytes;  // workspace offsets (partial sums of h first)
+    size_t h, perm, tiles, n_tiles, bytes;  // workspace offsets
 };
 
-size_t expand_smem(int R, coli_dtype ot)
-{
-    return (size_t)(ot == COLI_BF16 ? 2 : 3) * kLoTile * ((R + 31) / 32 * 32 + 8) * 2;
-}
-
-LoPlan lo_plan(const coli_adapters* d, int T)
+// How a call is cut, from the shapes and the output's type alone.
+LoPlan lo_plan(const coli_adapters* d, int T, coli_dtype ot)
 {
     LoPlan p{};
-    // tiles of T tokens over g groups: at most T / 64 whole ones and one more per group
-    p.max_tiles = std::max(1, T / kLoTile + std::min(T, d->n_adapters + 1));
-    // pieces of K that give about two blocks per SM, each with at least one 32-K block for every warp
-    const int most = std::max(1, d->in_features / (32 * kLoWarps));
-    p.pieces = std::max(1, std::min(most, 2 * kSms / p.max_tiles));
-    p.chunk = ((d->in_features + p.pieces - 1) / p.pieces + 32 * kLoWarps - 1) / (32 * kLoWarps) * (32 * kLoWarps);
-    p.pieces = (d->in_features + p.chunk - 1) / p.chunk;
-    // columns per block: as many as leave about four blocks per SM, whole rounds of the warps' 32
-    const int units = (d->out_features + 32 * kLoWarps - 1) / (32 * kLoWarps);
-    const int want = std::max(1, std::min(units, 4 * kSms / p.max_tiles));
-    p.cols = (units + want - 1) / want * 32 * kLoWarps;
-    size_t off = align_up((size_t)p.pieces * T * d->max_rank * 4, 256);
+    const int K = d->in_features, N = d->out_features;
+    auto up = [](int v, int m) { return (v + m - 1) / m * m; };
+    if (T <= kLoSmallT) {
+        p.max_tiles = std::max(1, std::min(T, d->n_adapters + 1));
+        // pieces of K that give about two blocks per SM, each with at least one 32-K block for every warp
+        const int most = std::max(1, K / (32 * kLoWarps));
+        p.pieces = std::max(1, std::min(most, 2 * kSms / p.max_tiles));
+        p.chunk = up((K + p.pieces - 1) / p.pieces, 32 * kLoWarps);
+        // columns per block: as many as leave about four blocks per SM, whole rounds of the warps' 32
+        const int units = (N + 32 * kLoWarps - 1) / (32 * kLoWarps);
+        const int want = std::max(1, std::min(units, 4 * kSms / p.max_tiles));
+        p.cols = (units + want - 1) / want * 32 * kLoWarps;
+    } else {
+        // tiles of T tokens over g groups: at most T / 128 whole ones and one more per group
+        p.max_tiles = T / kLtTile + std::min(T, d->n_adapters + 1);
+        // about one block per SM; fp32 outputs cut K at 512, which keeps what the tensor core drops per
+        // accumulation (2^-24.9 of a sum) below 2^-19.9
+        p.pieces = std::max(1, std::min(K / 256, kSms / p.max_tiles));
+        if (ot == COLI_F32) p.pieces = std::max(p.pieces, (K + 511) / 512);
+        p.chunk = up((K + p.pieces - 1) / p.pieces, 64);
+        const int step = 128, units = (N + step - 1) / step;
+        const int want = std::max(1, std::min(units, kSms / p.max_tiles));
+        p.cols = (units + want - 1) / want * step;
+    }
+    p.pieces = (K + p.chunk - 1) / p.chunk;
+    size_t off = kStatusBytes;
+    p.h = off;
+    off += align_up((size_t)p.pieces * T * d->max_rank * 4, 256);
     const bool big = T > kLoSmallT;
     p.perm = off;
     off += align_up(big ? (size_t)T * 4 : 0, 256);
@@ -64,6 +79,27 @@ LoPlan lo_plan(const coli_adapters* d, int T)
     return p;
 }
 
+size_t lo_expand_smem(int R, coli_dtype ot)
+{
+    return (size_t)(ot == COLI_BF16 ? 2 : 3) * kLoTile * ((R + 31) / 32 * 32 + 8) * 2;
+}
+
+template <bool kX16>
+cudaError_t launch_tc_shrink(const LoArgs& a, dim3 grid, cudaStream_t s)
+{
+    const size_t smem = 1024 + (size_t)lt_shrink_stages<kX16>(a.R) * lt_shrink_stage<kX16>(a.R);
+    return launch_pdl(lt_shrink_kernel<kX16>, grid, kLtThreads, smem, s, a);
+}
+
+template <bool kO16, int kCols>
+coli_status launch_tc_expand(const LoArgs& a, dim3 grid, cudaStream_t s)
+{
+    const coli_status st = allow_smem_once<lt_expand_kernel<kO16, kCols>>(kLtSmemBudget);
+    if (st != COLI_OK) return st;
+    const cudaError_t e = launch_pdl(lt_expand_kernel<kO16, kCols>, grid, kLtThreads, LtExpand<kO16, kCols>::smem(a.R), s, a);
+    return e == cudaSuccess ? COLI_OK : cuda_fail(e, "adapter expand launch");
+}
+
 }  // namespace
 
 extern "C" {
@@ -71,7 +107,8 @@ extern "C" {
 size_t coli_adapters_workspace_size(const coli_adapters* d, int T)
 {
     if (check_adapters(d, T) != COLI_OK) return 0;
-    return lo_plan(d, T).bytes;
+    // the cut differs between output types; either fits
+    return std::max(lo_plan(d, T, COLI_F32).bytes, lo_plan(d, T, COLI_BF16).bytes);
 }
 
 coli_status coli_adapters_forward(const coli_adapters* d, const void* x, coli_dtype xt, int T, const int32_t* which,
@@ -91,14 +128,17 @@ coli_status coli_adapters_forward(const coli_adapters* d, const void* x, coli_dt
     const size_t nx = (size_t)T * d->in_features * dtype_size(xt), no = (size_t)T * d->out_features * dtype_size(ot);
     if (overlap(x, nx, out, no)) return fail(COLI_ERR_INVALID_ARG, "out overlaps x");
     if (base != out && overlap(base, no, out, no)) return fail(COLI_ERR_INVALID_ARG, "out overlaps base without being the same tensor");
-    const LoPlan p = lo_plan(d, T);
-    if (ws_bytes < p.bytes) return fail(COLI_ERR_WORKSPACE, "workspace %zu bytes, need %zu", ws_bytes, p.bytes);
+    const LoPlan p = lo_plan(d, T, ot);
+    const size_t need = coli_adapters_workspace_size(d, T);
+    if (ws_bytes < need) return fail(COLI_ERR_WORKSPACE, "workspace %zu bytes, need %zu", ws_bytes, need);
 
     char* ws = static_cast<char*>(workspace);
     LoArgs a{};
     a.T = T, a.K = d->in_features, a.N = d->out_features, a.R = d->max_rank, a.n = d->n_adapters;
     a.x = x, a.a = d->a, a.b = d->b, a.rank = d->rank, a.scale = d->scale, a.which = which, a.base = base, a.out = out;
-    a.h = reinterpret_cast<float*>(ws);
+    a.status = reinterpret_cast<int*>(ws);
+    a.wait_ns = wait_limit(kLtWaitNs);
+    a.h = reinterpret_cast<float*>(ws + p.h);
     a.pieces = p.pieces, a.chunk = p.chunk, a.cols = p.cols, a.max_tiles = p.max_tiles;
     a.perm = reinterpret_cast<int32_t*>(ws + p.perm);
     a.tiles = reinterpret_cast<int32_t*>(ws + p.tiles);
@@ -107,18 +147,25 @@ coli_status coli_adapters_forward(const coli_adapters* d, const void* x, coli_dt
     cudaError_t e = cudaSuccess;
     const dim3 g1(p.max_tiles, p.pieces), g2(p.max_tiles, (a.N + a.cols - 1) / a.cols);
     if (T > kLoSmallT) {
+        st = xt == COLI_BF16 ? allow_smem_once<lt_shrink_kernel<true>>(kLtSmemBudget)
+                             : allow_smem_once<lt_shrink_kernel<false>>(kLtSmemBudget);
+        if (st != COLI_OK) return st;
         if ((e = launch_pdl(lo_group_kernel, dim3(1), kLoGroupThreads, 0, stream, a)) != cudaSuccess)
             return cuda_fail(e, "adapter grouping launch");
+        e = xt == COLI_BF16 ? launch_tc_shrink<true>(a, g1, stream) : launch_tc_shrink<false>(a, g1, stream);
+        if (e != cudaSuccess) return cuda_fail(e, "adapter shrink launch");
+        if (ot == COLI_BF16) return launch_tc_expand<true, 128>(a, g2, stream);
+        return a.R <= 192 ? launch_tc_expand<false, 64>(a, g2, stream) : launch_tc_expand<false, 32>(a, g2, stream);
     }
     if ((st = xt == COLI_BF16 ? allow_smem_once<lo_shrink_kernel<true>>((int)LoShrink<true>::kSmem)
                               : allow_smem_once<lo_shrink_kernel<false>>((int)LoShrink<false>::kSmem)) != COLI_OK ||
-        (st = ot == COLI_BF16 ? allow_smem_once<lo_expand_kernel<true>>((int)expand_smem(kLoMaxRank, ot))
-                              : allow_smem_once<lo_expand_kernel<false>>((int)expand_smem(kLoMaxRank, ot))) != COLI_OK)
+        (st = ot == COLI_BF16 ? allow_smem_once<lo_expand_kernel<true>>((int)lo_expand_smem(kLoMaxRank, ot))
+                              : allow_smem_once<lo_expand_kernel<false>>((int)lo_expand_smem(kLoMaxRank, ot))) != COLI_OK)
         return st;
     e = xt == COLI_BF16 ? launch_pdl(lo_shrink_kernel<true>, g1, kLoThreads, LoShrink<true>::kSmem, stream, a)
                         : launch_pdl(lo_shrink_kernel<false>, g1, kLoThreads, LoShrink<false>::kSmem, stream, a);
     if (e != cudaSuccess) return cuda_fail(e, "adapter shrink launch");
-    const size_t smem = expand_smem(a.R, ot);
+    const size_t smem = lo_expand_smem(a.R, ot);
     e = ot == COLI_BF16 ? launch_pdl(lo_expand_kernel<true>, g2, kLoThreads, smem, stream, a)
                         : launch_pdl(lo_expand_kernel<false>, g2, kLoThreads, smem, stream, a);
     return e == cudaSuccess ? COLI_OK : cuda_fail(e, "adapter expand launch");

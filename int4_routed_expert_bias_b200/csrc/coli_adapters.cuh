@@ -3,25 +3,24 @@
 //   out_t = base_t + scale_a B_a (A_a x_t),  a = the adapter of token t
 // A_a is [rank, K], B_a is [N, rank], bf16; tokens without an adapter keep base.
 //
-// Tokens are grouped into tiles of up to 64 of one adapter, so each adapter is
-// read once per tile.  Two kernels:
-//   shrink   h = A_a x for (tile, piece of K): the warps take 32-K blocks, their
-//            sums meet in shared memory, one fp32 partial row per piece
+// Tokens are grouped into tiles of one adapter, so each adapter is read once per
+// tile.  Two kernels:
+//   shrink   h = A_a x for (tile, piece of K), one fp32 partial row per piece
 //   expand   out for (tile, columns): the pieces of h are summed in order, scaled,
-//            cut into bf16 parts; each warp multiplies them with 32 rows of B_a at
-//            a time and adds base
-// A warp works on 32 tokens; in a tile of more, pairs of warps share the adapter's
-// rows (the second read finds them in L1).  The expand kernel starts while the
-// shrink kernel runs and has its first rows of B and base on the way before it
-// waits for h.
+//            cut into bf16 parts, multiplied with B_a and added to base
+// The expand kernel starts while the shrink kernel runs and has its first rows of B
+// and base on the way before it waits for h.  Memory-bound: at 4096 tokens,
+// K = N = 6144, rank 64 the arithmetic is 6.4 GFLOP against 176 MB, 4 us of tensor
+// work beside 27 us of traffic.
 //
-// Memory-bound: at 4096 tokens, K = N = 6144, rank 64 the arithmetic is 6.4 GFLOP
-// against 176 MB, 4 us of tensor work beside 27 us of traffic, so the products run
-// on warp-level mma (m16n8k16, fp32 accumulation) whose operands come straight
-// from global memory: K (and the rank) may be summed in any order, so lane q of a
-// quad takes 8 consecutive values of each 32, one 16-byte load that serves two
-// MMAs, and the output columns are dealt so that a lane ends with 8 consecutive
-// ones.  No staging of x, A or B.
+// This file: grouping, and the kernels for batches of up to 64 tokens (tiles of up
+// to 64), where latency counts.  Their products run on warp-level mma (m16n8k16,
+// fp32 accumulation) whose operands come straight from global memory: K (and the
+// rank) may be summed in any order, so lane q of a quad takes 8 consecutive values
+// of each 32, one 16-byte load that serves two MMAs, and the output columns are
+// dealt so that a lane ends with 8 consecutive ones; no staging of x, A or B.  A
+// warp works on 32 tokens; in a tile of more, pairs of warps share the adapter's
+// rows.  Larger batches: coli_adapters_tc.cuh.
 //
 // fp32 activations enter as three exact bf16 parts.  h is cut into three parts
 // for fp32 outputs (exact) and two for bf16 outputs (8 bits cut, 8 rounded: 2^-16
@@ -32,7 +31,8 @@
 
 namespace coli {
 
-constexpr int kLoTile = 64;      // tokens per tile
+constexpr int kLoTile = 64;      // tokens per tile of a small batch
+constexpr int kLtTile = 128;     // and of a large one
 constexpr int kLoRows = 32;      // tokens of a warp
 constexpr int kLoThreads = 256;
 constexpr int kLoWarps = kLoThreads / 32;
@@ -57,6 +57,8 @@ struct LoArgs {
     int32_t* tiles;          // [3 max_tiles] adapter, first position, count
     int32_t* n_tiles;        // [1]
     int max_tiles;
+    int* status;             // the call's status word
+    unsigned long long wait_ns;
 };
 
 // The adapter of a token; anything outside [0, n) is none (n).
@@ -91,7 +93,7 @@ __global__ void __launch_bounds__(kLoGroupThreads) lo_group_kernel(const __grid_
     int base_c = 0, base_t = 0;
     for (int b0 = 0; b0 < bins; b0 += kLoGroupThreads) {
         const int b = b0 + threadIdx.x;
-        const int c = b < bins ? count[b] : 0, nt = (c + kLoTile - 1) / kLoTile;
+        const int c = b < bins ? count[b] : 0, nt = (c + kLtTile - 1) / kLtTile;
         int ic = c, it = nt;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -111,14 +113,14 @@ __global__ void __launch_bounds__(kLoGroupThreads) lo_group_kernel(const __grid_
             for (int i = 0; i < nt; ++i) {
                 int32_t* e = a.tiles + 3 * (tile0[b] + i);
                 e[0] = b;
-                e[1] = first[b] + i * kLoTile;
-                e[2] = min(kLoTile, c - i * kLoTile);
+                e[1] = first[b] + i * kLtTile;
+                e[2] = min(kLtTile, c - i * kLtTile);
             }
         }
         base_c += all_c, base_t += all_t;
         __syncthreads();
     }
-    if (threadIdx.x == 0) *a.n_tiles = base_t;
+    if (threadIdx.x == 0) *a.n_tiles = base_t, *a.status = 0;
 #pragma unroll 4
     for (int t0 = warp * 32; t0 < a.T; t0 += kLoGroupThreads) {
         const int t = t0 + lane;
@@ -140,20 +142,12 @@ struct LoTile {
     uint32_t leaders[2];
 };
 
-// Fills `s` for tile number `tile`; false when there is no such tile.  Small
-// batches are grouped here, one tile per adapter in order of its first token;
-// large ones were grouped by lo_group_kernel.  All threads call it.
+// Fills `s` for tile number `tile` of a batch of up to 64 tokens, one tile per
+// adapter in order of its first token; false when there is no such tile.  All
+// threads call it.
 __device__ __forceinline__ bool lo_find_tile(const LoArgs& a, int tile, LoTile& s)
 {
     const int tid = threadIdx.x;
-    if (a.T > kLoSmallT) {
-        if (tile >= *a.n_tiles) return false;
-        const int32_t* e = a.tiles + 3 * tile;
-        if (tid == 0) s.adapter = e[0], s.count = e[2];
-        if (tid < kLoTile) s.token[tid] = a.perm[e[1] + min(tid, e[2] - 1)];  // the tail repeats a token
-        __syncthreads();
-        return true;
-    }
     int w = -1;
     if (tid < kLoSmallT) s.of[tid] = w = tid < a.T ? lo_adapter(a, tid) : -1;
     __syncthreads();
@@ -224,6 +218,7 @@ __global__ void __launch_bounds__(kLoThreads, 2) lo_shrink_kernel(const __grid_c
     extern __shared__ __align__(16) float sum[];  // [kLoWarps][kSlot]
     griddep_wait();
     griddep_launch_dependents();
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.status = 0;  // nothing waits in these kernels
     if (!lo_find_tile(a, blockIdx.x, s) || s.adapter == a.n) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const int ad = s.adapter, rank = a.rank ? min(max(a.rank[ad], 0), a.R) : a.R;

@@ -1,0 +1,543 @@
+// coli_adapters_tc.cuh -- the adapters' two products on the 5th-generation tensor
+// cores, for batches that lo_group_kernel has grouped (see coli_adapters.cuh for
+// the operator and for the kernels of small batches).
+//
+// The arithmetic is far below what the tensor cores can do; what they save is
+// instructions: with warp-level mma every 16-byte piece of x, A, B and base passes
+// through registers, and at 4096 tokens (K = N = 6144, rank 64) the kernels spent
+// 43 + 63 us issuing 12 and 18 million warp instructions.  Here a tile is 128 tokens
+// of one adapter, operands go from global to swizzled shared memory with
+// cp.async (rows gathered by token; what lies behind the rank, K or N is filled
+// with zeros by the copy itself), one thread issues tcgen05.mma, base comes the
+// same way as the operands, and out leaves through its buffers in whole lines.
+// (Bulk copies row by row, 256 bytes each, measured 4 us a step of 128 rows.)
+#pragma once
+
+#include "coli_adapters.cuh"
+#include "coli_tcgen05.cuh"
+
+namespace coli {
+
+
+constexpr int kLtPlane = kLtTile * 128;  // bytes of 64 K values (bf16) of a tile
+constexpr int kLtProducers = 256;
+constexpr int kLtThreads = kLtProducers + 32;  // and the MMA warp
+constexpr int kLtMaxStages = 6;
+constexpr int kLtSmemBudget = 232448 - 4096;   // static shared memory, alignment
+constexpr unsigned long long kLtWaitNs = 2000000000ull;   // 2 s: far beyond any legitimate wait
+constexpr unsigned long long kLtDrainNs = 100000000ull;   // teardown waits
+
+// 16 bytes global -> shared, of which `bytes` are read and the rest is zero.
+__device__ __forceinline__ void cp_async16_fill(uint32_t smem, const void* gmem, int bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem), "r"(bytes) : "memory");
+}
+// The barrier is arrived at when this thread's cp.async copies so far have landed
+// (one of the arrivals that it was initialised for).
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+struct LtTile {
+    int adapter, count;
+    int token[kLtTile];
+};
+
+// All threads call it; false when there is no such tile (for the whole block).
+__device__ __forceinline__ bool lt_find_tile(const LoArgs& a, int tile, LtTile& s)
+{
+    if (tile >= *a.n_tiles) return false;
+    const int32_t* e = a.tiles + 3 * tile;
+    if (threadIdx.x == 0) s.adapter = e[0], s.count = e[2];
+    if (threadIdx.x < kLtTile) s.token[threadIdx.x] = a.perm[e[1] + min((int)threadIdx.x, e[2] - 1)];  // the tail repeats a token
+    __syncthreads();
+    return true;
+}
+
+__host__ __device__ __forceinline__ int lt_rank16(int R) { return (R + 15) & ~15; }
+// Columns of TMEM: a power of two of at least 32.
+__host__ __device__ __forceinline__ int lt_cols(int n)
+{
+    int c = 32;
+    while (c < n) c *= 2;
+    return c;
+}
+
+// Shrink.  Stage: the tile's 64 K values in 1 or 3 parts, then those of R16 rows of A.
+template <bool kX16>
+__host__ __device__ __forceinline__ int lt_shrink_stage(int R)
+{
+    return (kX16 ? 1 : 3) * kLtPlane + lt_rank16(R) * 128;
+}
+// As many stages as leave room for a second block on the SM, but at least four
+// (bf16; two for fp32 x) where the whole of it is needed for them.
+template <bool kX16>
+__host__ __device__ __forceinline__ int lt_shrink_stages(int R)
+{
+    const int half = 110 * 1024 / lt_shrink_stage<kX16>(R), all = (kLtSmemBudget - 1024) / lt_shrink_stage<kX16>(R);
+    const int least = all < 4 ? all : 4;
+    return half < least ? least : half < kLtMaxStages ? half : kLtMaxStages;
+}
+
+// h[t, r] of one piece of K: D[128, R16] = X[128, piece] A^T.  Grid (tiles, pieces).
+// fp32 x: three exact parts, the first into one accumulator, the other two into a
+// second, added at the end.  Pieces are short (lo_plan), so what the tensor core
+// cuts off at each accumulation stays below 1e-6 of a sum.
+template <bool kX16>
+__global__ void __launch_bounds__(kLtThreads, 2) lt_shrink_kernel(const __grid_constant__ LoArgs a)
+{
+    constexpr int kParts = kX16 ? 1 : 3;
+    extern __shared__ __align__(16) unsigned char lt_smem_raw[];
+    unsigned char* smem =
+        reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(lt_smem_raw) + 1023) & ~(uintptr_t)1023);
+    __shared__ LtTile s;
+    __shared__ uint64_t full[kLtMaxStages], empty[kLtMaxStages], done;
+    __shared__ uint32_t tmem_base;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    griddep_wait();
+    if (!lt_find_tile(a, blockIdx.x, s) || s.adapter == a.n) {
+        griddep_launch_dependents();
+        return;
+    }
+    const int ad = s.adapter, rank = a.rank ? min(max(a.rank[ad], 0), a.R) : a.R;
+    if (rank == 0) {
+        griddep_launch_dependents();
+        return;
+    }
+    const int R16 = lt_rank16(a.R), n16 = lt_rank16(rank);
+    const int stages = lt_shrink_stages<kX16>(a.R), stage_bytes = lt_shrink_stage<kX16>(a.R);
+    const int cols = lt_cols((kX16 ? 1 : 2) * R16);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < stages; ++i) {
+            // every producer's copies, and for fp32 x the producer warps' own stores
+            mbar_init(&full[i], kLtProducers + (kX16 ? 0 : kLtProducers / 32));
+            mbar_init(&empty[i], 1);
+        }
+        mbar_init(&done, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kLtProducers / 32) tmem_alloc(&tmem_base, cols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    griddep_launch_dependents();  // after the allocation: a dependent never holds TMEM that this grid still needs
+    const uint32_t tmem = tmem_base;
+    const unsigned long long deadline = global_ns() + a.wait_ns;
+    const int k0 = blockIdx.y * a.chunk, k1 = min(a.K, k0 + a.chunk), steps = (k1 - k0 + 63) / 64;
+    const uint32_t smem0 = smem_u32(smem);
+
+    if (warp < kLtProducers / 32) {
+        const int c8 = threadIdx.x & 7, r0 = threadIdx.x >> 3;
+        const uint16_t* arow = a.a + ((size_t)ad * a.R + r0) * a.K + k0 + 8 * c8;
+        const uint32_t dst0 = r0 * 128 + ((c8 ^ (r0 & 7)) << 4);  // rows r0 + 32 i are swizzled alike
+        const char* xr[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            xr[i] = static_cast<const char*>(a.x) + ((size_t)s.token[r0 + 32 * i] * a.K + k0 + 8 * c8) * (kX16 ? 2 : 4);
+        auto copy_a = [&](int j) {
+            const bool kin = k0 + 64 * j + 8 * c8 < k1;
+            const uint32_t st = smem0 + (uint32_t)(j % stages) * stage_bytes + kParts * kLtPlane + dst0;
+            for (int i = 0; r0 + 32 * i < n16; ++i) {
+                const bool in = kin && r0 + 32 * i < rank;
+                cp_async16_fill(st + 32 * 128 * i, in ? arow + (size_t)32 * i * a.K + 64 * j : a.a, in ? 16 : 0);
+            }
+        };
+        auto wait_empty = [&](int j) {
+            bool ok = true;
+            if (j >= stages) ok = mbar_wait(&empty[j % stages], ((j / stages) - 1) & 1, deadline, a.status);
+            return (bool)__all_sync(0xFFFFFFFFu, ok);
+        };
+        if constexpr (kX16) {
+            for (int j = 0; j < steps; ++j) {
+                if (!wait_empty(j)) break;
+                const bool kin = k0 + 64 * j + 8 * c8 < k1;
+                const uint32_t st = smem0 + (uint32_t)(j % stages) * stage_bytes + dst0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const bool in = kin && r0 + 32 * i < s.count;
+                    cp_async16_fill(st + 32 * 128 * i, in ? xr[i] + (size_t)128 * j : a.x, in ? 16 : 0);
+                }
+                copy_a(j);
+                cp_async_arrive(&full[j % stages]);
+            }
+        } else {
+            // x through registers, one step ahead; A's copy of a step is under way for one step too
+            float v[4][8];
+            auto load_x = [&](int j) {
+                const bool kin = k0 + 64 * j + 8 * c8 < k1;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float4 w0 = make_float4(0.f, 0.f, 0.f, 0.f), w1 = w0;
+                    if (kin && r0 + 32 * i < s.count) {
+                        const float4* p = reinterpret_cast<const float4*>(xr[i] + (size_t)256 * j);
+                        w0 = p[0], w1 = p[1];
+                    }
+                    v[i][0] = w0.x, v[i][1] = w0.y, v[i][2] = w0.z, v[i][3] = w0.w;
+                    v[i][4] = w1.x, v[i][5] = w1.y, v[i][6] = w1.z, v[i][7] = w1.w;
+                }
+            };
+            auto copy_step = [&](int j) {
+                copy_a(j);
+                cp_async_arrive(&full[j % stages]);
+            };
+            bool ok = true;
+            load_x(0);
+            copy_step(0);
+            for (int j = 0; j < steps && ok; ++j) {
+                unsigned char* st = smem + (size_t)(j % stages) * stage_bytes + dst0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                    for (int u = 0; u < 3; ++u) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) w[c] = cut_pair(v[i][2 * c], v[i][2 * c + 1]);
+                        *reinterpret_cast<uint4*>(st + u * kLtPlane + 32 * 128 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[j % stages]);
+                if (j + 1 < steps) {
+                    load_x(j + 1);
+                    ok = wait_empty(j + 1);
+                    if (ok) copy_step(j + 1);
+                }
+            }
+        }
+        cp_async_wait_all();  // nothing is under way when the block ends
+    } else if (lane == 0) {
+        const uint32_t id = idesc_bf16(n16);
+        for (int j = 0; j < steps; ++j) {
+            if (!mbar_wait(&full[j % stages], (j / stages) & 1, deadline, a.status)) break;
+            fence_async_smem();  // the copies went through the generic proxy
+            tc_fence_after();
+            const uint32_t xs = smem0 + (uint32_t)(j % stages) * stage_bytes, as = xs + kParts * kLtPlane;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                const uint64_t bd = smem_desc_sw128(as + kk * 32);
+                tc_mma_ss(tmem, smem_desc_sw128(xs + kk * 32), bd, id, (j | kk) != 0);
+                if constexpr (!kX16) {
+                    tc_mma_ss(tmem + R16, smem_desc_sw128(xs + kLtPlane + kk * 32), bd, id, (j | kk) != 0);
+                    tc_mma_ss(tmem + R16, smem_desc_sw128(xs + 2 * kLtPlane + kk * 32), bd, id, 1);
+                }
+            }
+            tc_commit(&empty[j % stages]);
+        }
+        tc_commit(&done);
+    }
+    if (warp < 4) {
+        const bool ok = mbar_wait(&done, 0, deadline, a.status);
+        if (__all_sync(0xFFFFFFFFu, ok)) {
+            tc_fence_after();
+            const int row = warp * 32 + lane;
+            float* hp = a.h + ((size_t)blockIdx.y * a.T + s.token[row]) * a.R;
+            for (int c = 0; c < n16; c += 16) {
+                float v[16];
+                tmem_ld16(tmem + ((uint32_t)(warp * 32) << 16) + c, v);
+                if constexpr (!kX16) {
+                    float v1[16];
+                    tmem_ld16(tmem + ((uint32_t)(warp * 32) << 16) + R16 + c, v1);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] += v1[i];
+                }
+                if (row < s.count) {
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4)
+                        if (c + i < a.R) *reinterpret_cast<float4*>(hp + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                }
+            }
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == kLtProducers / 32) {
+        if (lane == 0) mbar_wait(&done, 0, global_ns() + kLtDrainNs, a.status);
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, cols);
+    }
+}
+
+// Expand.  Shared memory: the parts of scale h ([kParts][R / 64 rounded up] tiles of
+// 64 rank values), a ring of B tiles (64 rank values of the columns of a step), and
+// a ring of buffers of base rows, which become the output rows.
+template <bool kO16, int kCols>
+struct LtExpand {
+    static constexpr int kParts = kO16 ? 2 : 3;
+    static constexpr int kRowPitch = kCols * (kO16 ? 2 : 4) + 16;  // rows of a buffer start on other banks
+    static constexpr int kBStage = kCols * 128;
+    static constexpr int kBuf = kLtTile * kRowPitch;
+    static __host__ __device__ __forceinline__ int blocks(int R) { return (R + 63) / 64; }
+    static __host__ __device__ __forceinline__ int h_bytes(int R) { return kParts * blocks(R) * kLtPlane; }
+    // buffers of base rows, up to four, beside at least three B tiles (or what the highest ranks leave)
+    static __host__ __device__ __forceinline__ int buffers(int R)
+    {
+        const int n = (kLtSmemBudget - 1024 - h_bytes(R) - 3 * kBStage) / kBuf;
+        return n < 1 ? 1 : n < 4 ? n : 4;
+    }
+    static __host__ __device__ __forceinline__ int stages(int R)
+    {
+        const int n = (kLtSmemBudget - 1024 - h_bytes(R) - buffers(R) * kBuf) / kBStage;
+        return n < 4 ? n : 4;
+    }
+    static __host__ __device__ __forceinline__ size_t smem(int R)
+    {
+        return 1024 + (size_t)h_bytes(R) + (size_t)stages(R) * kBStage + (size_t)buffers(R) * kBuf;
+    }
+};
+
+// out = base + (scale h) B^T for a tile and `cols` columns.  Grid (tiles, column blocks).
+// Warps 0-3: a thread owns a token's row of the accumulator, adds it to base in the
+// buffer, and its warp writes its 32 rows out; warps 4-5 bring base, 6-7 B; all
+// eight build the parts of h.
+// kCols: columns of a step, 256 bytes of every row (32 columns for fp32 outputs of
+// the highest ranks, whose three parts of h take most of the shared memory).
+template <bool kO16, int kCols>
+__global__ void __launch_bounds__(kLtThreads, 1) lt_expand_kernel(const __grid_constant__ LoArgs a)
+{
+    using S = LtExpand<kO16, kCols>;
+    constexpr int kParts = S::kParts, es = kO16 ? 2 : 4, kLanes = kCols * es / 16;  // lanes of a row's 16-byte pieces
+    extern __shared__ __align__(16) unsigned char lt_smem_raw[];
+    unsigned char* smem =
+        reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(lt_smem_raw) + 1023) & ~(uintptr_t)1023);
+    __shared__ LtTile s;
+    __shared__ uint64_t full[4], empty[4], acc_full[2], acc_empty[2], base_full[4], base_empty[4], done;
+    __shared__ uint32_t tmem_base;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // Everything but h was complete before the shrink kernel let this one start.
+    const bool found = lt_find_tile(a, blockIdx.x, s);
+    if (!found || (s.adapter == a.n && a.base == a.out)) {  // in place: nothing to add
+        griddep_wait();
+        return;
+    }
+    const int ad = s.adapter;
+    const int rank = ad == a.n ? 0 : a.rank ? min(max(a.rank[ad], 0), a.R) : a.R;
+    const int nb = S::blocks(rank), stages = S::stages(a.R), bufs = S::buffers(a.R);
+    const int c0 = blockIdx.y * a.cols, c_end = min(a.N, c0 + a.cols), tiles = (c_end - c0 + kCols - 1) / kCols;
+    unsigned char* bring = smem + S::h_bytes(a.R);
+    unsigned char* rows = bring + stages * S::kBStage;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < stages; ++i) {
+            mbar_init(&full[i], 64);  // the threads that bring B
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], 4);  // epilogue warps
+        }
+        for (int i = 0; i < bufs; ++i) {
+            mbar_init(&base_full[i], 64);  // the threads that bring base
+            mbar_init(&base_empty[i], 4);
+        }
+        mbar_init(&done, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    const int mt = threadIdx.x & 63;  // of the 64 threads that bring base, or B
+    // base of column tile i into buffer i % bufs: piece mt % kLanes of rows mt / kLanes, ...
+    auto copy_base = [&](int i) {
+        const int piece = mt % kLanes, col = c0 + i * kCols + piece * (16 / es);
+        const uint32_t buf = smem_u32(rows + (i % bufs) * S::kBuf) + 16 * piece;
+        if (col < c_end)
+            for (int t = mt / kLanes; t < s.count; t += 64 / kLanes)
+                cp_async16_fill(buf + t * S::kRowPitch, static_cast<const char*>(a.base) + ((size_t)s.token[t] * a.N + col) * es, 16);
+        cp_async_arrive(&base_full[i % bufs]);
+    };
+    // B: rows of column tile i, 64 rank values of block kb, as step i * nb + kb
+    auto copy_b = [&](int step) {
+        const int i = step / nb, kb = step - i * nb, c8 = mt & 7, r0 = mt >> 3, rr = 64 * kb + 8 * c8;
+        const uint32_t st = smem_u32(bring) + (uint32_t)(step % stages) * S::kBStage + r0 * 128 + ((c8 ^ r0) << 4);
+        const int bytes = min(16, max(0, 2 * (rank - rr)));  // behind the rank: zeros, whatever is there
+        const uint16_t* src = a.b + ((size_t)ad * a.N + c0 + i * kCols + r0) * a.R + rr;
+#pragma unroll
+        for (int q = 0; q < kCols / 8; ++q) {
+            const bool in = c0 + i * kCols + r0 + 8 * q < c_end && bytes > 0;
+            cp_async16_fill(st + 8 * q * 128, in ? src + (size_t)8 * q * a.R : a.b, in ? bytes : 0);
+        }
+        cp_async_arrive(&full[step % stages]);
+    };
+    const int steps = tiles * nb;
+    const int early_b = min(steps, stages), early_base = a.base ? min(tiles, bufs) : 0;  // before h is there
+    if (warp >= 6 && warp < 8)
+        for (int j = 0; j < early_b; ++j) copy_b(j);
+    if (warp >= 4 && warp < 6)
+        for (int i = 0; i < early_base; ++i) copy_base(i);
+    const float scale = rank > 0 ? a.scale[ad] : 0.f;
+    griddep_wait();
+    if (warp == kLtProducers / 32) tmem_alloc(&tmem_base, 2 * kCols);
+    if (rank > 0 && warp < 8) {
+        const int chunks = nb * 8;  // 8 rank values each
+        const size_t plane = (size_t)a.T * a.R;
+        for (int e = threadIdx.x; e < kLtTile * chunks; e += kLtProducers) {
+            const int t = e / chunks, c = e - t * chunks, r = 8 * c;
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = 0.f;
+            if (t < s.count && r < rank) {
+                const float* hp = a.h + (size_t)s.token[t] * a.R + r;
+                for (int p0 = 0; p0 < a.pieces; p0 += 4) {  // eight independent loads at a time
+                    float4 o[4][2];
+#pragma unroll
+                    for (int p = 0; p < 4; ++p)
+                        if (p0 + p < a.pieces) {
+                            o[p][0] = *reinterpret_cast<const float4*>(hp + (p0 + p) * plane);
+                            o[p][1] = *reinterpret_cast<const float4*>(hp + (p0 + p) * plane + 4);
+                        }
+#pragma unroll
+                    for (int p = 0; p < 4; ++p)
+                        if (p0 + p < a.pieces) {
+                            v[0] += o[p][0].x, v[1] += o[p][0].y, v[2] += o[p][0].z, v[3] += o[p][0].w;
+                            v[4] += o[p][1].x, v[5] += o[p][1].y, v[6] += o[p][1].z, v[7] += o[p][1].w;
+                        }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = r + i < rank ? v[i] * scale : 0.f;
+            }
+            unsigned char* dst = smem + (c >> 3) * kLtPlane + t * 128 + (((c & 7) ^ (t & 7)) << 4);
+#pragma unroll
+            for (int u = 0; u < kParts; ++u) {
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (kO16 && u == kParts - 1) {  // the last of two parts is rounded, not cut
+                        const __nv_bfloat162 x = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                        w[i] = *reinterpret_cast<const uint32_t*>(&x);
+                    } else {
+                        w[i] = cut_pair(v[2 * i], v[2 * i + 1]);
+                    }
+                }
+                *reinterpret_cast<uint4*>(dst + (size_t)u * S::blocks(a.R) * kLtPlane) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+        fence_async_smem();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base;
+    const unsigned long long deadline = global_ns() + a.wait_ns;
+
+    if (warp >= 6 && warp < 8) {
+        // ---------------- B ----------------
+        for (int j = early_b; j < steps; ++j) {
+            const bool ok = mbar_wait(&empty[j % stages], ((j / stages) - 1) & 1, deadline, a.status);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            copy_b(j);
+        }
+        cp_async_wait_all();
+    } else if (warp >= 4 && warp < 6) {
+        // ---------------- base ----------------
+        for (int i = early_base; a.base && i < tiles; ++i) {
+            const bool ok = mbar_wait(&base_empty[i % bufs], ((i / bufs) - 1) & 1, deadline, a.status);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            copy_base(i);
+        }
+        cp_async_wait_all();
+    } else if (warp == kLtProducers / 32) {
+        // ---------------- MMA issuer ----------------
+        if (lane == 0 && rank > 0) {
+            const uint32_t id = idesc_bf16(kCols);
+            bool ok = true;
+            for (int i = 0; i < tiles && ok; ++i) {
+                const int buf = i & 1;
+                if (i >= 2) {
+                    ok = mbar_wait(&acc_empty[buf], ((i >> 1) - 1) & 1, deadline, a.status);
+                    if (!ok) break;
+                    tc_fence_after();
+                }
+                for (int kb = 0; kb < nb; ++kb) {
+                    const int j = i * nb + kb;
+                    ok = mbar_wait(&full[j % stages], (j / stages) & 1, deadline, a.status);
+                    if (!ok) break;
+                    fence_async_smem();  // the copies went through the generic proxy
+                    tc_fence_after();
+                    const uint32_t bs = smem_u32(bring) + (uint32_t)(j % stages) * S::kBStage;
+                    const int ks = min(4, (rank - 64 * kb + 15) / 16);
+                    for (int kk = 0; kk < ks; ++kk) {
+                        const uint64_t bd = smem_desc_sw128(bs + kk * 32);
+#pragma unroll
+                        for (int u = kParts - 1; u >= 0; --u)  // small parts first
+                            tc_mma_ss(tmem + buf * kCols, smem_desc_sw128(smem_u32(smem) + (u * S::blocks(a.R) + kb) * kLtPlane + kk * 32),
+                                      bd, id, kb > 0 || kk > 0 || u < kParts - 1);
+                    }
+                    tc_commit(&empty[j % stages]);
+                }
+                if (ok) tc_commit(&acc_full[buf]);
+            }
+            tc_commit(&done);
+        }
+    } else if (warp < 4) {
+        // ---------------- sums added to base, rows out ----------------
+        const int row = warp * 32 + lane;
+        for (int i = 0; i < tiles; ++i) {
+            const int b = i % bufs;
+            bool ok = !a.base || mbar_wait(&base_full[b], (i / bufs) & 1, deadline, a.status);
+            if (rank > 0) ok = mbar_wait(&acc_full[i & 1], (i >> 1) & 1, deadline, a.status) && ok;
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            tc_fence_after();
+            unsigned char* buf = rows + b * S::kBuf;
+            if (rank > 0 || !a.base) {
+                unsigned char* rp = buf + row * S::kRowPitch;
+#pragma unroll 2
+                for (int c = 0; c < kCols; c += 16) {
+                    float v[16];
+                    if (rank > 0) {
+                        tmem_ld16(tmem + ((uint32_t)(warp * 32) << 16) + (i & 1) * kCols + c, v);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) v[e] = 0.f;
+                    }
+                    uint4* q = reinterpret_cast<uint4*>(rp + c * es);
+                    if constexpr (kO16) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint4 o = make_uint4(0u, 0u, 0u, 0u);
+                            if (a.base) o = q[h];
+                            uint32_t w[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const __nv_bfloat162 x = __floats2bfloat162_rn(v[8 * h + 2 * e] + __uint_as_float(w[e] << 16),
+                                                                               v[8 * h + 2 * e + 1] + __uint_as_float(w[e] & 0xFFFF0000u));
+                                w[e] = *reinterpret_cast<const uint32_t*>(&x);
+                            }
+                            q[h] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                            float4* f = reinterpret_cast<float4*>(q + h);
+                            if (a.base) o = *f;
+                            *f = make_float4(o.x + v[4 * h], o.y + v[4 * h + 1], o.z + v[4 * h + 2], o.w + v[4 * h + 3]);
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_empty[i & 1]);
+            // this warp's rows, whole lines at a time
+            const int piece = lane % kLanes, col = c0 + i * kCols + piece * (16 / es);
+            if (col < c_end) {
+                char* out = static_cast<char*>(a.out) + (size_t)col * es;
+#pragma unroll 4
+                for (int t = warp * 32 + lane / kLanes; t < min(warp * 32 + 32, s.count); t += 32 / kLanes)
+                    *reinterpret_cast<uint4*>(out + (size_t)s.token[t] * a.N * es) =
+                        *reinterpret_cast<const uint4*>(buf + t * S::kRowPitch + 16 * piece);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&base_empty[b]);
+        }
+    }
+    __syncthreads();
+    if (warp == kLtProducers / 32) {
+        if (lane == 0 && rank > 0) mbar_wait(&done, 0, global_ns() + kLtDrainNs, a.status);
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 2 * kCols);
+    }
+}
+
+}  // namespace coli

@@ -208,12 +208,12 @@ route_gemm_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant_
         status = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    griddep_wait();  // before the allocation: TMEM is not held while waiting for a kernel that may need it
     if (warp == kRgWarpMma) tmem_alloc(&tmem_base, kRgTmemCols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base;
-    griddep_wait();
     const unsigned long long deadline = global_ns() + wait_ns;
 
     if (warp < kRgWarpEpi) {
