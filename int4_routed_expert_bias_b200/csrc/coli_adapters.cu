@@ -96,7 +96,7 @@ coli_status launch_tc_expand(const LoArgs& a, dim3 grid, cudaStream_t s)
 {
     const coli_status st = allow_smem_once<lt_expand_kernel<kO16, kCols>>(kLtSmemBudget);
     if (st != COLI_OK) return st;
-    const cudaError_t e = launch_pdl(lt_expand_kernel<kO16, kCols>, grid, kLtThreads, LtExpand<kO16, kCols>::smem(a.R), s, a);
+    const cudaError_t e = launch_pdl(lt_expand_kernel<kO16, kCols>, grid, kLtExpThreads, LtExpand<kO16, kCols>::smem(a.R), s, a);
     return e == cudaSuccess ? COLI_OK : cuda_fail(e, "adapter expand launch");
 }
 

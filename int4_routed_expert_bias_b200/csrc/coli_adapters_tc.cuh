@@ -23,6 +23,8 @@ constexpr int kLtPlane = kLtTile * 128;  // bytes of 64 K values (bf16) of a til
 constexpr int kLtProducers = 256;
 constexpr int kLtThreads = kLtProducers + 32;  // and the MMA warp
 constexpr int kLtMaxStages = 6;
+constexpr int kLtExpThreads = 256 + 6 * 32 + 32;  // expand: sums and rows, base and B, MMA
+constexpr int kLtWarpMma = kLtExpThreads / 32 - 1;
 constexpr int kLtSmemBudget = 232448 - 4096;   // static shared memory, alignment
 constexpr unsigned long long kLtWaitNs = 2000000000ull;   // 2 s: far beyond any legitimate wait
 constexpr unsigned long long kLtDrainNs = 100000000ull;   // teardown waits
@@ -289,22 +291,24 @@ struct LtExpand {
 };
 
 // out = base + (scale h) B^T for a tile and `cols` columns.  Grid (tiles, column blocks).
-// Warps 0-3: a thread owns a token's row of the accumulator, adds it to base in the
-// buffer, and its warp writes its 32 rows out; warps 4-5 bring base, 6-7 B; all
-// eight build the parts of h.
+// Warps 0-7 build the parts of h; then two warps share 32 rows: a thread adds its
+// half of a row of the accumulator to base in the buffer, and the two write the
+// rows out.  Warps 8-11 bring base, 12-13 B.
 // kCols: columns of a step, 256 bytes of every row (32 columns for fp32 outputs of
 // the highest ranks, whose three parts of h take most of the shared memory).
 template <bool kO16, int kCols>
-__global__ void __launch_bounds__(kLtThreads, 1) lt_expand_kernel(const __grid_constant__ LoArgs a)
+__global__ void __launch_bounds__(kLtExpThreads, 1) lt_expand_kernel(const __grid_constant__ LoArgs a)
 {
     using S = LtExpand<kO16, kCols>;
     constexpr int kParts = S::kParts, es = kO16 ? 2 : 4, kLanes = kCols * es / 16;  // lanes of a row's 16-byte pieces
+    constexpr int kTmem = 2 * kCols, kHalf = kCols / 2;  // two accumulators; a thread's columns of one
     extern __shared__ __align__(16) unsigned char lt_smem_raw[];
     unsigned char* smem =
         reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(lt_smem_raw) + 1023) & ~(uintptr_t)1023);
     __shared__ LtTile s;
     __shared__ uint64_t full[4], empty[4], acc_full[2], acc_empty[2], base_full[4], base_empty[4], done;
     __shared__ uint32_t tmem_base;
+    __shared__ int fail_s[8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // Everything but h was complete before the shrink kernel let this one start.
     const bool found = lt_find_tile(a, blockIdx.x, s);
@@ -325,26 +329,41 @@ __global__ void __launch_bounds__(kLtThreads, 1) lt_expand_kernel(const __grid_c
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], 4);  // epilogue warps
+            mbar_init(&acc_empty[i], 8);  // epilogue warps
         }
         for (int i = 0; i < bufs; ++i) {
-            mbar_init(&base_full[i], 64);  // the threads that bring base
-            mbar_init(&base_empty[i], 4);
+            mbar_init(&base_full[i], 128);  // the threads that bring base
+            mbar_init(&base_empty[i], 8);
         }
         mbar_init(&done, 1);
+        for (int i = 0; i < 8; ++i) fail_s[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
-    const int mt = threadIdx.x & 63;  // of the 64 threads that bring base, or B
-    // base of column tile i into buffer i % bufs: piece mt % kLanes of rows mt / kLanes, ...
+    // base of column tile i into buffer i % bufs, by 128 threads: piece mb % kLanes of rows mb / kLanes, ...
+    // (their addresses are kept: looked up row by row, they cost 160 cycles each)
+    constexpr int kRowsOf = kLanes;  // rows of a thread, 128 / kLanes apart
+    const int mb = threadIdx.x & 127, piece_b = mb % kLanes;
+    const char* base_row[kRowsOf];
+    if (warp >= 8 && warp < 12) {
+#pragma unroll
+        for (int j = 0; j < kRowsOf; ++j) {
+            const int t = mb / kLanes + j * (128 / kLanes);
+            base_row[j] = t < s.count && a.base
+                              ? static_cast<const char*>(a.base) + ((size_t)s.token[t] * a.N + c0) * es + 16 * piece_b
+                              : nullptr;
+        }
+    }
     auto copy_base = [&](int i) {
-        const int piece = mt % kLanes, col = c0 + i * kCols + piece * (16 / es);
-        const uint32_t buf = smem_u32(rows + (i % bufs) * S::kBuf) + 16 * piece;
-        if (col < c_end)
-            for (int t = mt / kLanes; t < s.count; t += 64 / kLanes)
-                cp_async16_fill(buf + t * S::kRowPitch, static_cast<const char*>(a.base) + ((size_t)s.token[t] * a.N + col) * es, 16);
+        const uint32_t buf = smem_u32(rows + (i % bufs) * S::kBuf) + (mb / kLanes) * S::kRowPitch + 16 * piece_b;
+        if (c0 + i * kCols + piece_b * (16 / es) < c_end) {
+#pragma unroll
+            for (int j = 0; j < kRowsOf; ++j)
+                if (base_row[j]) cp_async16_fill(buf + j * (128 / kLanes) * S::kRowPitch, base_row[j] + (size_t)i * (kCols * es), 16);
+        }
         cp_async_arrive(&base_full[i % bufs]);
     };
+    const int mt = threadIdx.x & 63;  // of the 64 threads that bring B
     // B: rows of column tile i, 64 rank values of block kb, as step i * nb + kb
     auto copy_b = [&](int step) {
         const int i = step / nb, kb = step - i * nb, c8 = mt & 7, r0 = mt >> 3, rr = 64 * kb + 8 * c8;
@@ -360,17 +379,17 @@ __global__ void __launch_bounds__(kLtThreads, 1) lt_expand_kernel(const __grid_c
     };
     const int steps = tiles * nb;
     const int early_b = min(steps, stages), early_base = a.base ? min(tiles, bufs) : 0;  // before h is there
-    if (warp >= 6 && warp < 8)
+    if (warp >= 12 && warp < 14)
         for (int j = 0; j < early_b; ++j) copy_b(j);
-    if (warp >= 4 && warp < 6)
+    if (warp >= 8 && warp < 12)
         for (int i = 0; i < early_base; ++i) copy_base(i);
     const float scale = rank > 0 ? a.scale[ad] : 0.f;
     griddep_wait();
-    if (warp == kLtProducers / 32) tmem_alloc(&tmem_base, 2 * kCols);
+    if (warp == kLtWarpMma) tmem_alloc(&tmem_base, kTmem);
     if (rank > 0 && warp < 8) {
         const int chunks = nb * 8;  // 8 rank values each
         const size_t plane = (size_t)a.T * a.R;
-        for (int e = threadIdx.x; e < kLtTile * chunks; e += kLtProducers) {
+        for (int e = threadIdx.x; e < kLtTile * chunks; e += 256) {
             const int t = e / chunks, c = e - t * chunks, r = 8 * c;
             float v[8];
 #pragma unroll
@@ -419,7 +438,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lt_expand_kernel(const __grid_c
     const uint32_t tmem = tmem_base;
     const unsigned long long deadline = global_ns() + a.wait_ns;
 
-    if (warp >= 6 && warp < 8) {
+    if (warp >= 12 && warp < 14) {
         // ---------------- B ----------------
         for (int j = early_b; j < steps; ++j) {
             const bool ok = mbar_wait(&empty[j % stages], ((j / stages) - 1) & 1, deadline, a.status);
@@ -427,7 +446,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lt_expand_kernel(const __grid_c
             copy_b(j);
         }
         cp_async_wait_all();
-    } else if (warp >= 4 && warp < 6) {
+    } else if (warp >= 8 && warp < 12) {
         // ---------------- base ----------------
         for (int i = early_base; a.base && i < tiles; ++i) {
             const bool ok = mbar_wait(&base_empty[i % bufs], ((i / bufs) - 1) & 1, deadline, a.status);
@@ -435,7 +454,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lt_expand_kernel(const __grid_c
             copy_base(i);
         }
         cp_async_wait_all();
-    } else if (warp == kLtProducers / 32) {
+    } else if (warp == kLtWarpMma) {
         // ---------------- MMA issuer ----------------
         if (lane == 0 && rank > 0) {
             const uint32_t id = idesc_bf16(kCols);
@@ -468,75 +487,101 @@ __global__ void __launch_bounds__(kLtThreads, 1) lt_expand_kernel(const __grid_c
             }
             tc_commit(&done);
         }
-    } else if (warp < 4) {
+    } else if (warp < 8) {
         // ---------------- sums added to base, rows out ----------------
-        const int row = warp * 32 + lane;
+        const int qd = warp & 3, half = warp >> 2, row = qd * 32 + lane;
+        // rows that this lane writes: qd * 32 + half + 2 (lane / kLanes), a step of 64 / kLanes apart
+        constexpr int kOut = kLanes / 2;  // of them
+        const int t0 = qd * 32 + 2 * (lane / kLanes) + half, piece = lane % kLanes;
+        const char* const src0 = reinterpret_cast<const char*>(rows) + t0 * S::kRowPitch + 16 * piece;
+        char* dst[kOut];
+#pragma unroll
+        for (int j = 0; j < kOut; ++j) {
+            const int t = t0 + j * (64 / kLanes);
+            dst[j] = t < s.count ? static_cast<char*>(a.out) + ((size_t)s.token[t] * a.N + c0) * es + 16 * piece : nullptr;
+        }
+        auto pair_sync = [&]() { asm volatile("barrier.cta.sync %0, 64;" ::"r"(1 + qd) : "memory"); };
         for (int i = 0; i < tiles; ++i) {
             const int b = i % bufs;
             bool ok = !a.base || mbar_wait(&base_full[b], (i / bufs) & 1, deadline, a.status);
             if (rank > 0) ok = mbar_wait(&acc_full[i & 1], (i >> 1) & 1, deadline, a.status) && ok;
-            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            if (!__all_sync(0xFFFFFFFFu, ok)) {
+                fail_s[warp] = 1;
+            }
             tc_fence_after();
-            unsigned char* buf = rows + b * S::kBuf;
             if (rank > 0 || !a.base) {
-                unsigned char* rp = buf + row * S::kRowPitch;
-#pragma unroll 2
-                for (int c = 0; c < kCols; c += 16) {
-                    float v[16];
-                    if (rank > 0) {
-                        tmem_ld16(tmem + ((uint32_t)(warp * 32) << 16) + (i & 1) * kCols + c, v);
-                    } else {
+                unsigned char* rp = rows + b * S::kBuf + row * S::kRowPitch + half * kHalf * es;
+                constexpr int kStep = kHalf < 32 ? kHalf : 32;
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) v[e] = 0.f;
-                    }
+                for (int c = 0; c < kHalf; c += kStep) {
+                    float v[kStep];
                     uint4* q = reinterpret_cast<uint4*>(rp + c * es);
-                    if constexpr (kO16) {
+                    constexpr int kPieces = kStep * es / 16;
+                    uint4 o[kPieces];
+                    if constexpr (kStep == 32) {
+                        uint32_t r[32];
+                        if (rank > 0) tmem_ld32_async(tmem + ((uint32_t)(qd * 32) << 16) + (i & 1) * kCols + half * kHalf + c, r);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint4 o = make_uint4(0u, 0u, 0u, 0u);
-                            if (a.base) o = q[h];
-                            uint32_t w[4] = {o.x, o.y, o.z, o.w};
+                        for (int h = 0; h < kPieces; ++h) {
+                            o[h] = make_uint4(0u, 0u, 0u, 0u);
+                            if (a.base) o[h] = q[h];
+                        }
+                        if (rank > 0) tmem_wait_ld(r);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
+                        for (int e = 0; e < 32; ++e) v[e] = rank > 0 ? __uint_as_float(r[e]) : 0.f;
+                    } else {
+                        static_assert(kStep == 16, "16 or 32 columns at a time");
+                        float r[16];
+                        if (rank > 0) tmem_ld16(tmem + ((uint32_t)(qd * 32) << 16) + (i & 1) * kCols + half * kHalf + c, r);
+#pragma unroll
+                        for (int h = 0; h < kPieces; ++h) {
+                            o[h] = make_uint4(0u, 0u, 0u, 0u);
+                            if (a.base) o[h] = q[h];
+                        }
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) v[e] = rank > 0 ? r[e] : 0.f;
+                    }
+#pragma unroll
+                    for (int h = 0; h < kPieces; ++h) {
+                        uint32_t w[4] = {o[h].x, o[h].y, o[h].z, o[h].w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if constexpr (kO16) {
                                 const __nv_bfloat162 x = __floats2bfloat162_rn(v[8 * h + 2 * e] + __uint_as_float(w[e] << 16),
                                                                                v[8 * h + 2 * e + 1] + __uint_as_float(w[e] & 0xFFFF0000u));
                                 w[e] = *reinterpret_cast<const uint32_t*>(&x);
+                            } else {
+                                w[e] = __float_as_uint(__uint_as_float(w[e]) + v[4 * h + e]);
                             }
-                            q[h] = make_uint4(w[0], w[1], w[2], w[3]);
                         }
-                    } else {
-#pragma unroll
-                        for (int h = 0; h < 4; ++h) {
-                            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                            float4* f = reinterpret_cast<float4*>(q + h);
-                            if (a.base) o = *f;
-                            *f = make_float4(o.x + v[4 * h], o.y + v[4 * h + 1], o.z + v[4 * h + 2], o.w + v[4 * h + 3]);
-                        }
+                        q[h] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
             }
             tc_fence_before();
-            __syncwarp();
+            pair_sync();  // both halves of the 32 rows are in the buffer
+            if (fail_s[qd] || fail_s[qd + 4]) break;  // uniform over the two warps
             if (lane == 0) mbar_arrive(&acc_empty[i & 1]);
-            // this warp's rows, whole lines at a time
-            const int piece = lane % kLanes, col = c0 + i * kCols + piece * (16 / es);
-            if (col < c_end) {
-                char* out = static_cast<char*>(a.out) + (size_t)col * es;
-#pragma unroll 4
-                for (int t = warp * 32 + lane / kLanes; t < min(warp * 32 + 32, s.count); t += 32 / kLanes)
-                    *reinterpret_cast<uint4*>(out + (size_t)s.token[t] * a.N * es) =
-                        *reinterpret_cast<const uint4*>(buf + t * S::kRowPitch + 16 * piece);
+            if (c0 + i * kCols + piece * (16 / es) < c_end) {  // whole lines at a time
+                const char* src = src0 + b * S::kBuf;
+                uint4 o[kOut];
+#pragma unroll
+                for (int j = 0; j < kOut; ++j) o[j] = *reinterpret_cast<const uint4*>(src + j * (64 / kLanes) * S::kRowPitch);
+#pragma unroll
+                for (int j = 0; j < kOut; ++j)
+                    if (dst[j]) *reinterpret_cast<uint4*>(dst[j] + (size_t)i * (kCols * es)) = o[j];
             }
+            if (!a.base) pair_sync();  // (with base, the movers' wait on base_empty keeps the buffer)
             __syncwarp();
             if (lane == 0) mbar_arrive(&base_empty[b]);
         }
     }
     __syncthreads();
-    if (warp == kLtProducers / 32) {
+    if (warp == kLtWarpMma) {
         if (lane == 0 && rank > 0) mbar_wait(&done, 0, global_ns() + kLtDrainNs, a.status);
         __syncwarp();
         tc_fence_after();
-        tmem_dealloc(tmem, 2 * kCols);
+        tmem_dealloc(tmem, kTmem);
     }
 }
 
