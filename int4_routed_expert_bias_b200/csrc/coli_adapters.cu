@@ -56,9 +56,9 @@ LoPlan lo_plan(const coli_adapters* d, int T, coli_dtype ot)
     } else {
         // tiles of T tokens over g groups: at most T / 128 whole ones and one more per group
         p.max_tiles = T / kLtTile + std::min(T, d->n_adapters + 1);
-        // about one block per SM; fp32 outputs cut K at 512, which keeps what the tensor core drops per
-        // accumulation (2^-24.9 of a sum) below 2^-19.9
-        p.pieces = std::max(1, std::min(K / 256, kSms / p.max_tiles));
+        // about two blocks per SM (4096 tokens: 23 us, one block 27 us); fp32 outputs cut K at 512, which keeps
+        // what the tensor core drops per accumulation (2^-24.9 of a sum) below 2^-19.9
+        p.pieces = std::max(1, std::min(K / 256, 2 * kSms / p.max_tiles));
         if (ot == COLI_F32) p.pieces = std::max(p.pieces, (K + 511) / 512);
         p.chunk = up((K + p.pieces - 1) / p.pieces, 64);
         const int step = 128, units = (N + step - 1) / step;

@@ -69,24 +69,36 @@ __device__ __forceinline__ int lo_adapter(const LoArgs& a, int t)
 }
 
 // Tokens by adapter for large batches: a counting sort by one block (n + 1 bins,
-// the last for tokens without an adapter) and the table of tiles.  A warp adds
-// each distinct adapter of its 32 tokens once.  The order inside an adapter does
-// not matter to any result: every token's sums are its own.
+// the last for tokens without an adapter) and the table of tiles.  The order inside
+// an adapter is left to the atomics and does not matter to any result: every
+// token's sums are its own.  Up to 8192 tokens keep their adapter and their place
+// in registers between the two steps; larger batches look both up again.
+constexpr int kLoKeep = 8;
+
 __global__ void __launch_bounds__(kLoGroupThreads) lo_group_kernel(const __grid_constant__ LoArgs a)
 {
-    __shared__ int count[kMaxExperts + 1], first[kMaxExperts + 1], tile0[kMaxExperts + 1];
+    __shared__ int count[kMaxExperts + 1], first[kMaxExperts + 1];
     __shared__ int wsum[2][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, bins = a.n + 1;
     for (int i = threadIdx.x; i < bins; i += kLoGroupThreads) count[i] = 0;
     griddep_wait();
     griddep_launch_dependents();
-    __syncthreads();
+    const bool keep = a.T <= kLoKeep * kLoGroupThreads;
+    int mine[kLoKeep], place[kLoKeep];
+    if (keep) {
+#pragma unroll
+        for (int u = 0; u < kLoKeep; ++u) {
+            const int t = threadIdx.x + u * kLoGroupThreads;
+            mine[u] = t < a.T ? lo_adapter(a, t) : -1;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < kLoKeep; ++u)
+            if (mine[u] >= 0) place[u] = atomicAdd(&count[mine[u]], 1);
+    } else {
+        __syncthreads();
 #pragma unroll 4
-    for (int t0 = warp * 32; t0 < a.T; t0 += kLoGroupThreads) {
-        const int t = t0 + lane;
-        const int w = t < a.T ? lo_adapter(a, t) : -1;
-        const uint32_t same = __match_any_sync(0xFFFFFFFFu, w);
-        if (w >= 0 && lane == __ffs(same) - 1) atomicAdd(&count[w], __popc(same));
+        for (int t = threadIdx.x; t < a.T; t += kLoGroupThreads) atomicAdd(&count[lo_adapter(a, t)], 1);
     }
     __syncthreads();
     // exclusive sums of tokens and tiles over the bins, 1024 at a time
@@ -109,9 +121,8 @@ __global__ void __launch_bounds__(kLoGroupThreads) lo_group_kernel(const __grid_
         }
         if (b < bins) {
             first[b] = base_c + pc + ic - c;
-            tile0[b] = base_t + pt + it - nt;
             for (int i = 0; i < nt; ++i) {
-                int32_t* e = a.tiles + 3 * (tile0[b] + i);
+                int32_t* e = a.tiles + 3 * (base_t + pt + it - nt + i);
                 e[0] = b;
                 e[1] = first[b] + i * kLtTile;
                 e[2] = min(kLtTile, c - i * kLtTile);
@@ -121,16 +132,13 @@ __global__ void __launch_bounds__(kLoGroupThreads) lo_group_kernel(const __grid_
         __syncthreads();
     }
     if (threadIdx.x == 0) *a.n_tiles = base_t, *a.status = 0;
+    if (keep) {
+#pragma unroll
+        for (int u = 0; u < kLoKeep; ++u)
+            if (mine[u] >= 0) a.perm[first[mine[u]] + place[u]] = threadIdx.x + u * kLoGroupThreads;
+    } else {
 #pragma unroll 4
-    for (int t0 = warp * 32; t0 < a.T; t0 += kLoGroupThreads) {
-        const int t = t0 + lane;
-        const int w = t < a.T ? lo_adapter(a, t) : -1;
-        const uint32_t same = __match_any_sync(0xFFFFFFFFu, w);
-        const int leader = __ffs(same) - 1;
-        int at = 0;
-        if (w >= 0 && lane == leader) at = atomicAdd(&first[w], __popc(same));
-        at = __shfl_sync(0xFFFFFFFFu, at, leader) + __popc(same & ((1u << lane) - 1u));
-        if (w >= 0) a.perm[at] = t;
+        for (int t = threadIdx.x; t < a.T; t += kLoGroupThreads) a.perm[atomicAdd(&first[lo_adapter(a, t)], 1)] = t;
     }
 }
 
