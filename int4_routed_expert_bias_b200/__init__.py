@@ -190,14 +190,32 @@ def _check_tensor(t, name, shape, dtypes):
     raise ValueError(f"{name} is not contiguous")
 
 
+# What the calls below use of torch, filled by _use_torch() when the first
+# description (Router, BlockNorm, Adapters, Block) is made: a call of a few
+# microseconds should not look modules up.
+_CODES = {}  # dtype -> coli_dtype
+_REAL = ()
+_I32 = _F32T = None
+_device = _raw_stream = None
+
+
+def _use_torch():
+    global _REAL, _I32, _F32T, _device, _raw_stream
+    if not _CODES:
+        import torch
+        _CODES.update({torch.float32: F32, torch.bfloat16: BF16})
+        _REAL, _I32, _F32T = (torch.bfloat16, torch.float32), torch.int32, torch.float32
+        _device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
 def _stream_of(t, stream):
     """The stream of a call on tensor t: the given one, else the current one.  The
     C calls launch on the current device, so a tensor on another GPU is refused."""
-    import torch
-    if t.is_cuda and t.get_device() != torch._C._cuda_getDevice():
-        raise ValueError(f"tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    dev = t.get_device()
+    if dev >= 0 and dev != _device():
+        raise ValueError(f"tensor on {t.device}, but the current device is cuda:{_device()}")
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(t.get_device())
+        return _raw_stream(dev)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -208,10 +226,10 @@ class Router:
 
     def __init__(self, hidden, n_experts, top_k, w_router, sel_bias=None, score="sigmoid", n_group=1, topk_group=1,
                  group_top=2, renormalise=True, routed_scale=1.0):
-        import torch
-        _check_tensor(w_router, "w_router", (n_experts, hidden), (torch.float32,))
+        _use_torch()
+        _check_tensor(w_router, "w_router", (n_experts, hidden), (_F32T,))
         if sel_bias is not None:
-            _check_tensor(sel_bias, "sel_bias", (n_experts,), (torch.float32,))
+            _check_tensor(sel_bias, "sel_bias", (n_experts,), (_F32T,))
         self.tensors = dict(w_router=w_router, sel_bias=sel_bias)
         self.hidden, self.n_experts, self.top_k = hidden, n_experts, top_k
         self.struct = _RouterStruct(hidden, n_experts, top_k, SCORES[score], n_group, topk_group, group_top,
@@ -230,13 +248,14 @@ def router_workspace_size(router, T):
 def router_forward(router, x, topk_idx, topk_w, workspace, stream=None):
     """Route x [T, H]: topk_idx [T, k] int32 and topk_w [T, k] fp32 are written.
     The first 4 bytes of the workspace are the call's status word."""
-    import torch
     T = x.shape[0]
-    _check_tensor(x, "x", (T, router.hidden), (torch.bfloat16, torch.float32))
-    _check_tensor(topk_idx, "topk_idx", (T, router.top_k), (torch.int32,))
-    _check_tensor(topk_w, "topk_w", (T, router.top_k), (torch.float32,))
-    _check(_lib.coli_router_forward(router.ref, x.data_ptr(), _dtype_code(x), T, topk_idx.data_ptr(), topk_w.data_ptr(),
-                                    workspace.data_ptr(), workspace.nbytes, _stream_of(x, stream)))
+    _check_tensor(x, "x", (T, router.hidden), _REAL)
+    _check_tensor(topk_idx, "topk_idx", (T, router.top_k), (_I32,))
+    _check_tensor(topk_w, "topk_w", (T, router.top_k), (_F32T,))
+    st = _lib.coli_router_forward(router.ref, x.data_ptr(), _CODES[x.dtype], T, topk_idx.data_ptr(), topk_w.data_ptr(),
+                                  workspace.data_ptr(), workspace.nbytes, _stream_of(x, stream))
+    if st:
+        raise ColiError(st)
 
 
 GATES = {"none": 0, "channel": 1, "token": 2, "element": 3}
@@ -249,39 +268,49 @@ class BlockNorm:
 
     def __init__(self, hidden, post_w=None, pre_w=None, eps=1e-5, gate="none", gate_sigmoid=False, residual_scale=1.0,
                  block_scale=1.0):
-        import torch
+        _use_torch()
         for name, w in (("post_w", post_w), ("pre_w", pre_w)):
             if w is not None:
-                _check_tensor(w, name, (hidden,), (torch.float32,))
+                _check_tensor(w, name, (hidden,), (_F32T,))
         self.tensors = dict(post_w=post_w, pre_w=pre_w)
         self.hidden, self.gate = hidden, gate
         self.struct = _BlockNormStruct(hidden, float(eps), _ptr(post_w), _ptr(pre_w), GATES[gate],
                                        1 if gate_sigmoid else 0, float(residual_scale), float(block_scale))
         self.ref = ctypes.byref(self.struct)
 
+    def gate_shape(self, T):
+        """Shape of the gate of T tokens."""
+        if self.gate == "none":
+            raise ValueError("the norm has no gate")
+        return (T,) if self.gate == "token" else (self.hidden,) if self.gate == "channel" else (T, self.hidden)
+
 
 def residual_norm(norm, residual, block_out, residual_out, normed_out, gate=None, stream=None):
     """residual_out = residual_scale * residual + block_scale * gate * norm(block_out)
     and normed_out = norm(residual_out), each [T, H].  block_out, residual_out and
     normed_out may be None (see coli_residual_norm in include/coli.h)."""
-    import torch
-    T, H = residual.shape
-    real = (torch.bfloat16, torch.float32)
-    _check_tensor(residual, "residual", (T, norm.hidden), real)
-    xt = block_out if block_out is not None else normed_out if normed_out is not None else residual
+    shape = residual.shape
+    T = shape[0]
+    _check_tensor(residual, "residual", (T, norm.hidden), _REAL)
+    rt = residual.dtype
+    xt = block_out.dtype if block_out is not None else normed_out.dtype if normed_out is not None else rt
+    d = r = y = g = None
     if block_out is not None:
-        _check_tensor(block_out, "block_out", (T, H), real)
+        _check_tensor(block_out, "block_out", shape, _REAL)
+        d = block_out.data_ptr()
     if residual_out is not None:
-        _check_tensor(residual_out, "residual_out", (T, H), (residual.dtype,))
+        _check_tensor(residual_out, "residual_out", shape, (rt,))
+        r = residual_out.data_ptr()
     if normed_out is not None:
-        _check_tensor(normed_out, "normed_out", (T, H), (xt.dtype,))
+        _check_tensor(normed_out, "normed_out", shape, (xt,) if xt in _CODES else _REAL)
+        y = normed_out.data_ptr()
     if gate is not None:
-        shape = {"channel": (H,), "token": (T,), "element": (T, H)}.get(norm.gate)
-        if shape is None:
-            raise ValueError("the norm has no gate")
-        _check_tensor(gate, "gate", shape, (xt.dtype,))
-    _check(_lib.coli_residual_norm(norm.ref, _ptr(block_out), _dtype_code(xt), residual.data_ptr(), _dtype_code(residual),
-                                   _ptr(gate), T, _ptr(residual_out), _ptr(normed_out), _stream_of(residual, stream)))
+        _check_tensor(gate, "gate", norm.gate_shape(T), (xt,))
+        g = gate.data_ptr()
+    st = _lib.coli_residual_norm(norm.ref, d, _CODES[xt], residual.data_ptr(), _CODES[rt], g, T, r, y,
+                                 _stream_of(residual, stream))
+    if st:
+        raise ColiError(st)
 
 
 class Adapters:
@@ -290,14 +319,14 @@ class Adapters:
     include/coli.h."""
 
     def __init__(self, a, b, scale, rank=None):
-        import torch
+        _use_torch()
         n, R, K = a.shape
         N = b.shape[1]
-        _check_tensor(a, "a", (n, R, K), (torch.bfloat16,))
-        _check_tensor(b, "b", (n, N, R), (torch.bfloat16,))
-        _check_tensor(scale, "scale", (n,), (torch.float32,))
+        _check_tensor(a, "a", (n, R, K), _REAL[:1])
+        _check_tensor(b, "b", (n, N, R), _REAL[:1])
+        _check_tensor(scale, "scale", (n,), (_F32T,))
         if rank is not None:
-            _check_tensor(rank, "rank", (n,), (torch.int32,))
+            _check_tensor(rank, "rank", (n,), (_I32,))
         self.tensors = dict(a=a, b=b, scale=scale, rank=rank)
         self.in_features, self.out_features = K, N
         self.struct = _AdaptersStruct(K, N, R, n, _ptr(a), _ptr(b), _ptr(scale), _ptr(rank))
@@ -315,17 +344,19 @@ def adapters_workspace_size(adapters, T):
 def adapters_forward(adapters, x, which, out, workspace, base=None, stream=None):
     """out [T, N] = base [T, N] + the adapter which[t] of each row of x [T, K];
     which is int32 [T], outside [0, n) for no adapter.  base may be out or None."""
-    import torch
     T = x.shape[0]
-    real = (torch.bfloat16, torch.float32)
-    _check_tensor(x, "x", (T, adapters.in_features), real)
-    _check_tensor(which, "which", (T,), (torch.int32,))
-    _check_tensor(out, "out", (T, adapters.out_features), real)
+    _check_tensor(x, "x", (T, adapters.in_features), _REAL)
+    _check_tensor(which, "which", (T,), (_I32,))
+    _check_tensor(out, "out", (T, adapters.out_features), _REAL)
+    base_ptr = None
     if base is not None:
         _check_tensor(base, "base", (T, adapters.out_features), (out.dtype,))
-    _check(_lib.coli_adapters_forward(adapters.ref, x.data_ptr(), _dtype_code(x), T, which.data_ptr(), _ptr(base),
-                                      out.data_ptr(), _dtype_code(out), workspace.data_ptr(), workspace.nbytes,
-                                      _stream_of(x, stream)))
+        base_ptr = base.data_ptr()
+    st = _lib.coli_adapters_forward(adapters.ref, x.data_ptr(), _CODES[x.dtype], T, which.data_ptr(), base_ptr,
+                                    out.data_ptr(), _CODES[out.dtype], workspace.data_ptr(), workspace.nbytes,
+                                    _stream_of(x, stream))
+    if st:
+        raise ColiError(st)
 
 
 def expert_union(topk_idx, E, count, offset, active, n_active, perm, inv_perm, stream=None):
@@ -364,13 +395,12 @@ def moe_forward(layer, x, out, workspace, topk_idx_out=None, topk_w_out=None, st
 def moe_forward_routed(layer, x, topk_idx, topk_w, out, workspace, stream=None):
     """moe_forward with the routing given: topk_idx [T, k] int32 and topk_w [T, k]
     fp32, e.g. from router_forward; see include/coli.h."""
-    import torch
+    _use_torch()
     T = x.shape[0]
-    real = (torch.bfloat16, torch.float32)
-    _check_tensor(x, "x", (T, layer.hidden), real)
-    _check_tensor(topk_idx, "topk_idx", (T, layer.top_k), (torch.int32,))
-    _check_tensor(topk_w, "topk_w", (T, layer.top_k), (torch.float32,))
-    _check_tensor(out, "out", (T, layer.hidden), real)
+    _check_tensor(x, "x", (T, layer.hidden), _REAL)
+    _check_tensor(topk_idx, "topk_idx", (T, layer.top_k), (_I32,))
+    _check_tensor(topk_w, "topk_w", (T, layer.top_k), (_F32T,))
+    _check_tensor(out, "out", (T, layer.hidden), _REAL)
     _check(_lib.coli_moe_forward_routed(layer.ref, x.data_ptr(), _dtype_code(x), T, topk_idx.data_ptr(), topk_w.data_ptr(),
                                         out.data_ptr(), _dtype_code(out), workspace.data_ptr(), workspace.nbytes,
                                         _stream_of(x, stream)))
@@ -381,6 +411,7 @@ class Block:
     of its own and adapters beside the layer; see coli_moe_block in include/coli.h."""
 
     def __init__(self, layer, norm_before, norm_after, router=None, adapters=None):
+        _use_torch()
         self.layer, self.norm_before, self.norm_after = layer, norm_before, norm_after
         self.router, self.adapters = router, adapters
         self.struct = _BlockStruct(*[None if m is None else ctypes.addressof(m.struct)
@@ -388,14 +419,9 @@ class Block:
         self.ref = ctypes.byref(self.struct)
 
 
-def _dtype_of(dtype):
-    import torch
-    return {torch.float32: F32, torch.bfloat16: BF16}[dtype]
-
-
 def moe_block_workspace_size(block, dtype, T):
     """Bytes of workspace moe_block_forward needs for T tokens of activations of a torch dtype."""
-    n = int(_lib.coli_moe_block_workspace_size(block.ref, _dtype_of(dtype), T))
+    n = int(_lib.coli_moe_block_workspace_size(block.ref, _CODES[dtype], T))
     if n == 0:
         raise ColiError(1)
     return n
@@ -404,7 +430,7 @@ def moe_block_workspace_size(block, dtype, T):
 def moe_block_status_word_offsets(block, dtype, T):
     """(router's, layer's) byte offsets of the status words in the workspace, None where there is none."""
     r, l = ctypes.c_size_t(), ctypes.c_size_t()
-    _check(_lib.coli_moe_block_status_word_offsets(block.ref, _dtype_of(dtype), T, ctypes.byref(r), ctypes.byref(l)))
+    _check(_lib.coli_moe_block_status_word_offsets(block.ref, _CODES[dtype], T, ctypes.byref(r), ctypes.byref(l)))
     return tuple(None if v.value == ctypes.c_size_t(-1).value else v.value for v in (r, l))
 
 
@@ -414,9 +440,8 @@ def moe_block_forward(block, residual, prev_out, residual_out, next_in, workspac
     normalised residual, its output into the residual, and next_in, the next
     block's input (None when norm_after has no pre_w).  The activations' dtype is
     prev_out's, or next_in's where prev_out is None; see include/coli.h."""
-    import torch
     T, H = residual.shape
-    real = (torch.bfloat16, torch.float32)
+    real = _REAL
     _check_tensor(residual, "residual", (T, block.layer.hidden), real)
     _check_tensor(residual_out, "residual_out", (T, H), (residual.dtype,))
     act = prev_out if prev_out is not None else next_in if next_in is not None else residual
@@ -426,12 +451,9 @@ def moe_block_forward(block, residual, prev_out, residual_out, next_in, workspac
         _check_tensor(next_in, "next_in", (T, H), (act.dtype,))
     for name, gate, norm in (("gate_before", gate_before, block.norm_before), ("gate_after", gate_after, block.norm_after)):
         if gate is not None:
-            shape = {"channel": (H,), "token": (T,), "element": (T, H)}.get(norm.gate)
-            if shape is None:
-                raise ValueError(f"{name}: the norm has no gate")
-            _check_tensor(gate, name, shape, (act.dtype,))
+            _check_tensor(gate, name, norm.gate_shape(T), (act.dtype,))
     if which is not None:
-        _check_tensor(which, "which", (T,), (torch.int32,))
+        _check_tensor(which, "which", (T,), (_I32,))
     _check(_lib.coli_moe_block_forward(block.ref, _ptr(prev_out), _dtype_code(act), residual.data_ptr(),
                                        _dtype_code(residual), _ptr(gate_before), _ptr(gate_after), _ptr(which), T,
                                        residual_out.data_ptr(), _ptr(next_in), workspace.data_ptr(), workspace.nbytes,
