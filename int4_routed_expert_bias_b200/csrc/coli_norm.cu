@@ -1,4 +1,5 @@
 // coli_norm.cu -- host side of the residual path around a block (coli_residual_norm).
+#include <algorithm>
 #include <cmath>
 
 #include "coli_host.h"
@@ -7,6 +8,10 @@
 using namespace coli;
 
 namespace {
+
+constexpr int kSms = 148;                    // grid sizing (B200)
+constexpr size_t kWalkFrom = (size_t)8 << 20;  // values of a batch from which blocks walk its rows
+constexpr int kMaxWalkVecs = 1024;
 
 template <bool kD, bool kR>
 cudaError_t launch(const NormArgs& a, cudaStream_t s)
@@ -19,7 +24,15 @@ cudaError_t launch(const NormArgs& a, cudaStream_t s)
         const int nv = a.H / 8;
         if (nv <= 32) return go(residual_norm_kernel<kD, kR, 8, 1, true>, eighth, 256);
         if (nv <= 64) return go(residual_norm_kernel<kD, kR, 8, 2, true>, eighth, 256);
-        return go(residual_norm_kernel<kD, kR, 8, 2, false>, a.T, ((nv + 1) / 2 + 31) / 32 * 32);
+        const int threads = ((nv + 1) / 2 + 31) / 32 * 32;
+        // Blocks that walk the rows with the next row's loads under way win for bf16 where the traffic does not stay in
+        // L2 and only one mean is reduced (4800 x 6144: 37.9 us, a block per row 44.7; 9600 x 2048: 25.7, 28.1).  With
+        // the norm of the block's output too, more blocks per SM hide its second reduction better (4800 x 8192: 76 us
+        // against 95), and fp32 rows keep enough bytes under way without (9600 x 6144, fp32 residual: 103 against 128).
+        if constexpr (kD && kR)
+            if (!a.post_w && nv <= kMaxWalkVecs && (size_t)a.T * a.H >= kWalkFrom)
+                return go(residual_norm_rows_kernel<2>, kSms * std::max(1, 800 / threads), threads);
+        return go(residual_norm_kernel<kD, kR, 8, 2, false>, a.T, threads);
     }
     if (a.H <= 128) return go(residual_norm_kernel<kD, kR, 1, 4, true>, eighth, 256);
     if (a.H <= 4096) return go(residual_norm_kernel<kD, kR, 1, 4, false>, a.T, ((a.H + 3) / 4 + 31) / 32 * 32);

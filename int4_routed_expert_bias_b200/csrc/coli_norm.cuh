@@ -84,28 +84,12 @@ __device__ __forceinline__ float row_sum(float v, float* red)
     return v;
 }
 
-// kD, kR: bf16 block output / residual.  kN vectors of kVec values per thread,
-// blockDim.x threads (kWarpRow: 32) side by side along the row.
+// One row held in d and r (kN vectors of kVec values per thread, `width` threads side by side).
 template <bool kD, bool kR, int kVec, int kN, bool kWarpRow>
-__global__ void __launch_bounds__(kWarpRow ? 256 : 1024) residual_norm_kernel(const __grid_constant__ NormArgs a)
+__device__ __forceinline__ void norm_row(const NormArgs& a, int t, int lane, int width, float (&d)[kN][kVec],
+                                         float (&r)[kN][kVec], float (*red)[32])
 {
-    __shared__ float red[2][32];
-    const int lane = kWarpRow ? threadIdx.x & 31 : threadIdx.x, width = kWarpRow ? 32 : blockDim.x;
-    const int t = kWarpRow ? blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
-    griddep_wait();
-    if (t >= a.T) return;  // whole warps (or none) leave
     const size_t row = (size_t)t * a.H;
-    float d[kN][kVec], r[kN][kVec];
-#pragma unroll
-    for (int n = 0; n < kN; ++n) {
-        const int i = (lane + n * width) * kVec;
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) d[n][j] = r[n][j] = 0.f;
-        if (i < a.H) {
-            if (a.d) load_vec<kD, kVec>(a.d, row + i, d[n]);
-            load_vec<kR, kVec>(a.r, row + i, r[n]);
-        }
-    }
     float f = a.block_scale;
     if (a.gate == kGateToken) {
         float g[1];
@@ -154,6 +138,70 @@ __global__ void __launch_bounds__(kWarpRow ? 256 : 1024) residual_norm_kernel(co
 #pragma unroll
         for (int j = 0; j < kVec; ++j) o[j] = r[n][j] * q * w[j];
         store_vec<kD, kVec>(a.y, row + i, o);
+    }
+}
+
+// kD, kR: bf16 block output / residual.  A block (or, kWarpRow, a warp) per row.
+template <bool kD, bool kR, int kVec, int kN, bool kWarpRow>
+__global__ void __launch_bounds__(kWarpRow ? 256 : 1024) residual_norm_kernel(const __grid_constant__ NormArgs a)
+{
+    __shared__ float red[2][32];
+    const int lane = kWarpRow ? threadIdx.x & 31 : threadIdx.x, width = kWarpRow ? 32 : blockDim.x;
+    const int t = kWarpRow ? blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+    griddep_wait();
+    if (t >= a.T) return;  // whole warps (or none) leave
+    float d[kN][kVec], r[kN][kVec];
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+        const int i = (lane + n * width) * kVec;
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) d[n][j] = r[n][j] = 0.f;
+        if (i < a.H) {
+            if (a.d) load_vec<kD, kVec>(a.d, (size_t)t * a.H + i, d[n]);
+            load_vec<kR, kVec>(a.r, (size_t)t * a.H + i, r[n]);
+        }
+    }
+    norm_row<kD, kR, kVec, kN, kWarpRow>(a, t, lane, width, d, r, red);
+}
+
+// Long bf16 batches: blocks walk the rows, the next row's loads under way while the
+// mean of the current one is reduced.
+template <int kN>
+__global__ void __launch_bounds__(512) residual_norm_rows_kernel(const __grid_constant__ NormArgs a)
+{
+    __shared__ float red[2][2][32];
+    griddep_wait();
+    uint4 pd[kN], pr[kN];  // the next row as it is stored
+    auto widen = [](const uint4& u, float (&v)[8]) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = __uint_as_float(w[j] << 16);
+            v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+        }
+    };
+    auto load = [&](int t) {
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+            const int i = (threadIdx.x + n * blockDim.x) * 8;
+            pd[n] = pr[n] = make_uint4(0u, 0u, 0u, 0u);
+            if (i < a.H) {
+                if (a.d) pd[n] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.d) + (size_t)t * a.H + i);
+                pr[n] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.r) + (size_t)t * a.H + i);
+            }
+        }
+    };
+    int t = blockIdx.x;
+    if (t < a.T) load(t);
+    for (int b = 0; t < a.T; t += gridDim.x, b ^= 1) {
+        float d[kN][8], r[kN][8];
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+            widen(pd[n], d[n]);
+            widen(pr[n], r[n]);
+        }
+        if (t + gridDim.x < a.T) load(t + gridDim.x);
+        norm_row<true, true, 8, kN, false>(a, t, threadIdx.x, blockDim.x, d, r, red[b]);
     }
 }
 

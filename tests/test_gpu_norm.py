@@ -95,6 +95,16 @@ def test_widths(env, T, H, xt, rt):
     check(env, T, H, xt, rt)
 
 
+@pytest.mark.parametrize("T,H", [(2049, 4096), (1200, 7000), (8200, 1032), (1025, 8192)])
+@pytest.mark.parametrize("xt,rt", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32"), ("f32", "bf16")])
+def test_long_batches(env, T, H, xt, rt):
+    """Batches whose rows are walked (no norm of the block's output), and the same with it."""
+    check(env, T, H, xt, rt, post=False, gate="channel", in_place=True)
+    check(env, T, H, xt, rt, post=False, pre=False, gate="element", sigmoid=True)
+    check(env, T, H, xt, rt, post=False, block=False, with_residual=False)
+    check(env, T, H, xt, rt, post=True)
+
+
 @pytest.mark.parametrize("H", [192, 77, 1536, 6000])
 @pytest.mark.parametrize("gate", ["none", "channel", "token", "element"])
 @pytest.mark.parametrize("sigmoid", [False, True])
