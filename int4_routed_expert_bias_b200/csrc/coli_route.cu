@@ -55,13 +55,14 @@ struct RoutePlan {
 // Batches from this size on take the tensor-core score kernel.
 constexpr int kRouteBatchMin = 9;
 
-RoutePlan route_plan(int T, int H, int E)
+RoutePlan route_plan(int T, int H, int E, coli_dtype xt)
 {
     RoutePlan p{};
     p.Ep = (E + 3) & ~3;
     p.batch = T >= kRouteBatchMin;
     if (p.batch) {
-        p.m_tiles = (T + kRgM - 1) / kRgM;
+        const int m = kRgM * (xt == COLI_BF16 ? RgShape<true>::kSets : RgShape<false>::kSets);
+        p.m_tiles = (T + m - 1) / m;
         p.e_tiles = (E + kRgMaxE - 1) / kRgMaxE;
         p.ET = ((E + p.e_tiles - 1) / p.e_tiles + 15) / 16 * 16;
         const int ksteps = (H + kRgK - 1) / kRgK, tiles = p.m_tiles * p.e_tiles;
@@ -105,7 +106,8 @@ cudaError_t launch_batch(const RouteArgs& a, const RoutePlan& p, cudaStream_t s)
     if (kBf16 && !encode_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.x, (uint64_t)a.H, (uint64_t)a.T, kRgK, kRgM,
                             CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
-    return launch_pdl(route_gemm_kernel<kBf16>, dim3(p.m_tiles, p.e_tiles, p.splits), kRgThreads, RgShape<kBf16>::kSmem, s,
+    return launch_pdl(route_gemm_kernel<kBf16>, dim3(p.m_tiles, p.e_tiles, p.splits), RgShape<kBf16>::kThreads,
+                      RgShape<kBf16>::kSmem, s,
                       tx, a, p.ET, wait_limit(kRgWaitNs));
 }
 
@@ -135,7 +137,8 @@ extern "C" {
 size_t coli_router_workspace_size(const coli_router* r, int T)
 {
     if (check_router(r, T) != COLI_OK) return 0;
-    return route_plan(T, r->hidden, r->n_experts).bytes;
+    // the cut differs between activation types; either fits
+    return std::max(route_plan(T, r->hidden, r->n_experts, COLI_F32).bytes, route_plan(T, r->hidden, r->n_experts, COLI_BF16).bytes);
 }
 
 coli_status coli_router_forward(const coli_router* r, const void* x, coli_dtype xt, int T, int32_t* topk_idx,
@@ -149,8 +152,9 @@ coli_status coli_router_forward(const coli_router* r, const void* x, coli_dtype 
     if (!aligned(x, 16)) return fail(COLI_ERR_INVALID_ARG, "x not 16-byte aligned");
     if (!aligned(topk_idx, 4) || !aligned(topk_w, 4)) return fail(COLI_ERR_INVALID_ARG, "routing outputs not 4-byte aligned");
     if (!aligned(workspace, 256)) return fail(COLI_ERR_INVALID_ARG, "workspace not 256-byte aligned");
-    const RoutePlan p = route_plan(T, r->hidden, r->n_experts);
-    if (ws_bytes < p.bytes) return fail(COLI_ERR_WORKSPACE, "workspace %zu bytes, need %zu", ws_bytes, p.bytes);
+    const RoutePlan p = route_plan(T, r->hidden, r->n_experts, xt);
+    const size_t need = coli_router_workspace_size(r, T);
+    if (ws_bytes < need) return fail(COLI_ERR_WORKSPACE, "workspace %zu bytes, need %zu", ws_bytes, need);
 
     RouteArgs a{};
     a.T = T, a.H = r->hidden, a.E = r->n_experts, a.k = r->top_k;

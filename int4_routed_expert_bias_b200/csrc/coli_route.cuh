@@ -105,49 +105,53 @@ __global__ void __launch_bounds__(kRouteThreads) route_rows_kernel(const __grid_
 }
 
 // ---------------------------------------------------------------------------
-// Scores, batch form: tensor cores.  Z[128 tokens, ET experts] += X . W^T over
-// one piece of K per CTA.  fp32 operands go in as sums of bf16 numbers: cutting
+// Scores, batch form: tensor cores.  Z[tokens, ET experts] += X . W^T over one
+// piece of K per CTA, for 256 tokens (bf16) or 128 (fp32).  fp32 operands go in as sums of bf16 numbers: cutting
 // an fp32 value after its top 16 bits gives a bf16 number, the rest is exact in
 // fp32 and is cut again, so v = v0 + v1 + v2 exactly, each |v(i+1)| < 2^-7 |v(i)|
 // (8 significant bits at a time).  A bf16 activation is its own first part.
 // The products x_i w_j with i + j <= 2 are kept; what is dropped is below
 // 2^-21 of |x||w| (bf16 activations drop nothing).
 //
-// The parts of W lie one behind another along the MMA's N, part 0 of all ET
-// experts, then part 1, then part 2.  The accumulator has columns for order 0
-// (products of first parts) and for orders 1 and 2 side by side, so one MMA over
-// N = 2 ET multiplies a part of x with two parts of W, and small terms meet
+// Order 0 (products of first parts) has accumulators of its own, small terms meet
 // large sums only in the epilogue.  The tensor core cuts what does not fit its
-// fp32 accumulator at every step (2.8e-6 of z over 192 steps, always towards
-// zero), so order 0 is collected over kRgRound steps at a time in one of two
-// column ranges, and the epilogue warps add finished ranges to the partial
-// scores in fp32 while the other range fills (measured: 2^-17.3 of the largest
-// |z| without, 2^-20 with).
+// fp32 accumulator at every step (2.8e-6 of z over 192 steps, always towards zero),
+// so order 0 is collected over kRgRound steps at a time, and the epilogue warps add
+// finished ranges to the partial scores in fp32 while the MMAs go on (measured:
+// 2^-17.3 of the largest |z| without, 2^-20 with).  Where the MMAs go on:
+//   bf16: two sets of 128 tokens share every part of W; their ranges end half a
+//         round apart, so while one set's order 0 is read the other set's products
+//         and the set's own small ones run;
+//   fp32: order 0 alternates between two column ranges.
 //
-// Roles: two halves of eight producer warps split fp32 operands into swizzled
-// shared memory, the next step's global loads in registers (bf16 activations:
-// the halves take alternate steps of W, TMA brings x; fp32: one half W, one x);
-// one thread issues MMAs, one TMA; four warps are the epilogue.  Bound by shared
-// memory: a 64-K step writes 64 KB and the MMAs read 80 KB, against 768 tensor
-// cycles.
+// Roles: eight producer warps split W (eight more fp32 x) into swizzled shared
+// memory, the next step's global loads in registers; TMA brings bf16 x; one thread
+// issues MMAs, one TMA; four warps are the epilogue.  Bound by shared
+// memory and the loads of W from L2, which all CTAs of an expert tile read: with
+// 128 bf16 tokens per CTA the scores of 4096 tokens took 63 us, with 256 (a W part
+// split once for twice the tokens) see the figure at the launch.
 constexpr int kRgM = 128, kRgK = 64;
-constexpr int kRgHalf = 256;                   // producer threads of one half
-constexpr int kRgProducers = 2 * kRgHalf;
-constexpr int kRgWarpEpi = kRgProducers / 32, kRgWarpMma = kRgWarpEpi + 4, kRgWarpTma = kRgWarpMma + 1;
-constexpr int kRgThreads = (kRgWarpTma + 1) * 32;
+constexpr int kRgHalf = 256;                   // producer threads of W, and of fp32 x
 constexpr int kRgMaxE = 128;                   // experts per CTA
 constexpr int kRgRound = 8;                    // 64-K steps that order 0 is collected over
+constexpr int kRgHalfRound = kRgRound / 2;
 constexpr int kRgPlaneA = kRgM * 128;          // bytes of one part of x in a stage
-constexpr int kRgTmemCols = 512, kRgO12 = 256; // columns: order 0 twice (0, 128), then orders 1 and 2
+constexpr int kRgTmemCols = 512, kRgO12 = 256; // fp32 x: order 0 twice (columns 0, 128), then orders 1 and 2 side by side
 constexpr unsigned long long kRgWaitNs = 2000000000ull;  // 2 s: far beyond any legitimate wait
 constexpr unsigned long long kRgDrainNs = 100000000ull;  // teardown waits
 
 template <bool kBf16>
 struct RgShape {
     static constexpr int kPartsX = kBf16 ? 1 : 3;
-    static constexpr int kStages = kBf16 ? 3 : 2;
-    static constexpr int kStageBytes = kPartsX * kRgPlaneA + 3 * kRgMaxE * 128;
-    static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes;
+    static constexpr int kSets = kBf16 ? 2 : 1;  // sets of 128 tokens
+    static constexpr int kStages = 2;
+    static constexpr int kProducers = kBf16 ? kRgHalf : 2 * kRgHalf;
+    static constexpr int kWarpEpi = kProducers / 32, kWarpMma = kWarpEpi + 4, kWarpTma = kWarpMma + 1;
+    static constexpr int kThreads = (kWarpTma + 1) * 32;
+    static constexpr int kXBytes = kSets * kPartsX * kRgPlaneA;
+    static constexpr int kStageBytes = kXBytes + 3 * kRgMaxE * 128;
+    static constexpr int kSide = kBf16 ? kRgM * kRgMaxE * 4 : 0;  // a set's scores on their way out, row-major
+    static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + kSide;
 };
 
 // Eight fp32 values -> eight bf16 of part 0, 1, 2 (16 bytes each), exact.
@@ -168,7 +172,7 @@ __device__ __forceinline__ void split8(float (&r)[8], unsigned char* dst, int pl
 }
 
 // Add four floats in L2 without waiting for them.  Each place here has one adding
-// thread, whose additions to it stay in program order: the sum is deterministic.
+// lane of one warp, whose additions to it stay in program order: the sum is deterministic.
 __device__ __forceinline__ void red_add4(float* p, float x, float y, float z, float w)
 {
     asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
@@ -177,7 +181,7 @@ __device__ __forceinline__ void red_add4(float* p, float x, float y, float z, fl
 // tx: bf16 x [T, H], boxes of 64 x 128 tokens, 128-byte swizzle (unused for fp32 x).
 // ET: experts of a CTA, a multiple of 16, at most 128.
 template <bool kBf16>
-__global__ void __launch_bounds__(kRgThreads, 1)
+__global__ void __launch_bounds__(RgShape<kBf16>::kThreads, 1)
 route_gemm_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ RouteArgs a, int ET,
                   unsigned long long wait_ns)
 {
@@ -190,14 +194,14 @@ route_gemm_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant_
     __shared__ int status;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int m0 = blockIdx.x * kRgM, e0 = blockIdx.y * ET;
+    const int m0 = blockIdx.x * (S::kSets * kRgM), e0 = blockIdx.y * ET;
+    const int sets = min(S::kSets, (a.T - m0 + kRgM - 1) / kRgM);  // sets with tokens
     const int k0 = blockIdx.z * a.chunk;
     const int k1 = min(a.H, k0 + a.chunk);
     const int steps = (k1 - k0 + kRgK - 1) / kRgK;
-    const int rounds = (steps + kRgRound - 1) / kRgRound;
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kStages; ++i) {
-            mbar_init(&full[i], kBf16 ? kRgHalf / 32 + 1 : kRgProducers / 32);  // producer warps (and the TMA thread)
+            mbar_init(&full[i], S::kProducers / 32 + (kBf16 ? 1 : 0));  // producer warps (and the TMA thread)
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -209,18 +213,17 @@ route_gemm_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant_
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     griddep_wait();  // before the allocation: TMEM is not held while waiting for a kernel that may need it
-    if (warp == kRgWarpMma) tmem_alloc(&tmem_base, kRgTmemCols);
+    if (warp == S::kWarpMma) tmem_alloc(&tmem_base, kRgTmemCols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base;
     const unsigned long long deadline = global_ns() + wait_ns;
 
-    if (warp < kRgWarpEpi) {
+    if (warp < S::kWarpEpi) {
         // ---------------- producers ----------------
         const int half = warp >> 3, tid = threadIdx.x & (kRgHalf - 1);
-        const bool is_x = !kBf16 && half == 1;
-        const int first = kBf16 ? half : 0, stride = kBf16 ? 2 : 1;
+        const bool is_x = half == 1;
         // 16-byte chunks (8 values) of a step: chunk tid & 7 of rows tid >> 3, + 32, ...
         const int c8 = tid & 7, r0 = tid >> 3;
         constexpr int kQ = kRgM * 8 / kRgHalf;  // 4
@@ -229,7 +232,7 @@ route_gemm_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant_
         const float* src = (is_x ? static_cast<const float*>(a.x) + (size_t)m0 * a.H : a.w_router + (size_t)e0 * a.H) +
                            (size_t)r0 * a.H + k0 + 8 * c8;
         const size_t row32 = (size_t)32 * a.H;
-        const int dst0 = (is_x ? 0 : S::kPartsX * kRgPlaneA) + r0 * 128 + ((c8 ^ (r0 & 7)) << 4);
+        const int dst0 = (is_x ? 0 : S::kXBytes) + r0 * 128 + ((c8 ^ (r0 & 7)) << 4);
         const int plane = is_x ? kRgPlaneA : ET * 128;
         float v[kQ][8];
         auto load = [&](int j) {
@@ -246,8 +249,8 @@ route_gemm_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant_
                 v[q][4] = w1.x, v[q][5] = w1.y, v[q][6] = w1.z, v[q][7] = w1.w;
             }
         };
-        if (first < steps) load(first);
-        for (int j = first; j < steps; j += stride) {
+        load(0);
+        for (int j = 0; j < steps; ++j) {
             const int s = j % S::kStages;
             bool ok = true;
             if (j >= S::kStages) ok = mbar_wait(&empty[s], ((j / S::kStages) - 1) & 1, deadline, &status);
@@ -259,71 +262,145 @@ route_gemm_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant_
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&full[s]);
-            if (j + stride < steps) load(j + stride);
+            if (j + 1 < steps) load(j + 1);
         }
-    } else if (warp == kRgWarpTma) {
+    } else if (warp == S::kWarpTma) {
         // ---------------- TMA: bf16 activations ----------------
         if (kBf16 && lane == 0) {
             int j = 0;
             for (; j < steps; ++j) {
                 const int s = j % S::kStages;
                 if (j >= S::kStages && !mbar_wait(&empty[s], ((j / S::kStages) - 1) & 1, deadline, &status)) break;
-                mbar_expect_tx(&full[s], kRgPlaneA);
-                tma_load_2d(smem + (size_t)s * S::kStageBytes, &tx, k0 + j * kRgK, m0, &full[s]);
+                mbar_expect_tx(&full[s], sets * kRgPlaneA);
+                for (int h = 0; h < sets; ++h)
+                    tma_load_2d(smem + (size_t)s * S::kStageBytes + h * kRgPlaneA, &tx, k0 + j * kRgK, m0 + h * kRgM, &full[s]);
             }
             // every issued copy lands before the CTA can retire (normally long done)
             const unsigned long long drain = global_ns() + kRgDrainNs;
             for (int i = max(0, j - S::kStages); i < j; ++i)
                 mbar_wait(&full[i % S::kStages], (i / S::kStages) & 1, drain, &status);
         }
-    } else if (warp == kRgWarpMma) {
+    } else if (warp == S::kWarpMma) {
         // ---------------- MMA issuer ----------------
         if (lane == 0) {
             const uint32_t n1 = idesc_bf16(ET), n2 = idesc_bf16(2 * ET);
-            for (int j = 0; j < steps; ++j) {
-                const int s = j % S::kStages, round = j / kRgRound, buf = round & 1;
-                if (j % kRgRound == 0 && round >= 2) {
-                    if (!mbar_wait(&acc_empty[buf], ((round >> 1) - 1) & 1, deadline, &status)) break;
-                    tc_fence_after();
-                }
-                if (!mbar_wait(&full[s], (j / S::kStages) & 1, deadline, &status)) break;
+            bool ok = true;
+            for (int j = 0; j < steps && ok; ++j) {
+                const int s = j % S::kStages;
+                ok = mbar_wait(&full[s], (j / S::kStages) & 1, deadline, &status);
+                if (!ok) break;
                 tc_fence_after();
-                const uint32_t xs = smem_u32(smem + (size_t)s * S::kStageBytes), ws = xs + S::kPartsX * kRgPlaneA;
-                const uint32_t o0 = tmem + buf * kRgMaxE, o12 = tmem + kRgO12;
+                const uint32_t xs = smem_u32(smem + (size_t)s * S::kStageBytes), ws = xs + S::kXBytes;
+                if constexpr (kBf16) {
+                    // columns of set h: order 0 at 256 h, orders 1 and 2 at 256 h + 128
+                    const int begins = j > 0 && j % kRgHalfRound == 0 ? (j / kRgHalfRound) & 1 : -1;  // set that begins a round here
+                    auto small = [&](int h) {
 #pragma unroll
-                for (int kk = 0; kk < kRgK / 16; ++kk) {
-                    const uint64_t x0 = smem_desc_sw128(xs + kk * 32), w0 = smem_desc_sw128(ws + kk * 32);
-                    const uint64_t w1 = smem_desc_sw128(ws + ET * 128 + kk * 32);
-                    tc_mma_ss(o0, x0, w0, n1, j % kRgRound != 0 || kk != 0);
-                    tc_mma_ss(o12, x0, w1, n2, (j | kk) != 0);
-                    if constexpr (!kBf16) {
+                        for (int kk = 0; kk < kRgK / 16; ++kk) {
+                            const uint64_t x = smem_desc_sw128(xs + h * kRgPlaneA + kk * 32);
+                            tc_mma_ss(tmem + 256 * h + kRgMaxE, x, smem_desc_sw128(ws + 2 * ET * 128 + kk * 32), n1, (j | kk) != 0);
+                            tc_mma_ss(tmem + 256 * h + kRgMaxE, x, smem_desc_sw128(ws + ET * 128 + kk * 32), n1, 1);
+                        }
+                    };
+                    auto large = [&](int h) {
+#pragma unroll
+                        for (int kk = 0; kk < kRgK / 16; ++kk)
+                            tc_mma_ss(tmem + 256 * h, smem_desc_sw128(xs + h * kRgPlaneA + kk * 32), smem_desc_sw128(ws + kk * 32),
+                                      n1, (j > 0 && begins != h) || kk > 0);
+                    };
+                    for (int h = 0; h < sets; ++h)
+                        if (h != begins) {
+                            large(h);
+                            small(h);
+                        }
+                    if (begins >= 0 && begins < sets) {
+                        small(begins);
+                        // round number r of set 0 begins at step 8 r, of set 1 at 8 r - 4
+                        const int r = (j + begins * kRgHalfRound) / kRgRound;
+                        ok = mbar_wait(&acc_empty[begins], (r - 1) & 1, deadline, &status);
+                        if (!ok) break;
+                        tc_fence_after();
+                        large(begins);
+                    }
+                    tc_commit(&empty[s]);
+                    if ((j + 1) % kRgHalfRound == 0 && j + 1 < steps) {
+                        const int h = ((j + 1) / kRgHalfRound) & 1;
+                        if (h < sets) tc_commit(&acc_full[h]);
+                    }
+                } else {
+                    const int round = j / kRgRound, buf = round & 1;
+                    if (j % kRgRound == 0 && round >= 2) {
+                        ok = mbar_wait(&acc_empty[buf], ((round >> 1) - 1) & 1, deadline, &status);
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
+                    const uint32_t o0 = tmem + buf * kRgMaxE, o12 = tmem + kRgO12;
+#pragma unroll
+                    for (int kk = 0; kk < kRgK / 16; ++kk) {
+                        const uint64_t x0 = smem_desc_sw128(xs + kk * 32), w0 = smem_desc_sw128(ws + kk * 32);
+                        tc_mma_ss(o0, x0, w0, n1, j % kRgRound != 0 || kk != 0);
+                        tc_mma_ss(o12, x0, smem_desc_sw128(ws + ET * 128 + kk * 32), n2, (j | kk) != 0);
                         tc_mma_ss(o12, smem_desc_sw128(xs + kRgPlaneA + kk * 32), w0, n2, 1);
                         tc_mma_ss(o12 + ET, smem_desc_sw128(xs + 2 * kRgPlaneA + kk * 32), w0, n1, 1);
                     }
+                    tc_commit(&empty[s]);
+                    if (j % kRgRound == kRgRound - 1 && j + 1 < steps) tc_commit(&acc_full[buf]);
                 }
-                tc_commit(&empty[s]);
-                if (j % kRgRound == kRgRound - 1 && j + 1 < steps) tc_commit(&acc_full[buf]);
             }
             tc_commit(&done);  // every MMA issued above completes before the last sums are read
         }
     } else {
-        // ---------------- epilogue (warps 16-19: TMEM lane quadrants 0-3) ----------------
-        const int qd = warp & 3, t = m0 + qd * 32 + lane;
+        // ---------------- epilogue (TMEM lane quadrant: warp mod 4) ----------------
+        const int qd = warp & 3;
         const uint32_t lanes = (uint32_t)(qd * 32) << 16;
-        float* out = a.part + ((size_t)blockIdx.z * a.T + t) * a.Ep + e0;
-        for (int r = 0; r < rounds; ++r) {
-            const bool last = r == rounds - 1;
-            const bool ok = last ? mbar_wait(&done, 0, deadline, &status)
-                                 : mbar_wait(&acc_full[r & 1], (r >> 1) & 1, deadline, &status);
-            if (!__all_sync(0xFFFFFFFFu, ok)) break;
-            tc_fence_after();
+        // bf16: a finished range of order 0 at column o0 (and what is at o12, if any) of set h goes to
+        // shared memory first, 16-byte pieces permuted by row; then the MMAs may have the columns again, and
+        // the rows leave in whole lines (lane by lane, 16 bytes of 32 rows at a time, the additions of a range
+        // took 4400 cycles)
+        auto drain = [&](int h, uint32_t o0, int o12, bool first, uint64_t* release) {
+            float* side = reinterpret_cast<float*>(smem + S::kStages * S::kStageBytes) + qd * 32 * kRgMaxE;
+            for (int q = 0; 32 * q < ET; ++q) {
+                uint32_t r[32];
+                tmem_ld32_async(tmem + lanes + o0 + 32 * q, r);
+                tmem_wait_ld(r);
+                if (o12 >= 0) {
+                    uint32_t r1[32];
+                    tmem_ld32_async(tmem + lanes + o12 + 32 * q, r1);
+                    tmem_wait_ld(r1);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(r1[i]));
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    *reinterpret_cast<uint4*>(side + lane * kRgMaxE + (((8 * q + i) ^ lane) << 2)) =
+                        make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (release && lane == 0) mbar_arrive(release);
+            const int t0 = m0 + h * kRgM + qd * 32;
+            if (4 * lane < ET && e0 + 4 * lane < a.Ep) {
+                float* out = a.part + ((size_t)blockIdx.z * a.T + t0) * a.Ep + e0 + 4 * lane;
+#pragma unroll 8
+                for (int r = 0; r < min(32, a.T - t0); ++r) {
+                    const float4 v = *reinterpret_cast<const float4*>(side + r * kRgMaxE + ((lane ^ r) << 2));
+                    if (first) *reinterpret_cast<float4*>(out + (size_t)r * a.Ep) = v;
+                    else red_add4(out + (size_t)r * a.Ep, v.x, v.y, v.z, v.w);
+                }
+            }
+            __syncwarp();
+        };
+        // fp32: straight from the accumulator, lane by lane
+        auto drain_direct = [&](uint32_t o0, int o12, bool first, uint64_t* release) {
+            const int t = m0 + qd * 32 + lane;
+            float* out = a.part + ((size_t)blockIdx.z * a.T + t) * a.Ep + e0;
             for (int c = 0; c < ET; c += 16) {
                 float v[16];
-                tmem_ld16(tmem + lanes + (r & 1) * kRgMaxE + c, v);
-                if (last) {
+                tmem_ld16(tmem + lanes + o0 + c, v);
+                if (o12 >= 0) {
                     float v1[16], v2[16];
-                    tmem_ld16(tmem + lanes + kRgO12 + c, v1);
-                    tmem_ld16(tmem + lanes + kRgO12 + ET + c, v2);
+                    tmem_ld16(tmem + lanes + o12 + c, v1);
+                    tmem_ld16(tmem + lanes + o12 + ET + c, v2);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) v[i] += v1[i] + v2[i];
                 }
@@ -331,19 +408,40 @@ route_gemm_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant_
 #pragma unroll
                     for (int i = 0; i < 16; i += 4)
                         if (e0 + c + i < a.Ep) {
-                            if (r == 0) *reinterpret_cast<float4*>(out + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                            if (first) *reinterpret_cast<float4*>(out + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                             else red_add4(out + c + i, v[i], v[i + 1], v[i + 2], v[i + 3]);
                         }
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (!last && lane == 0) mbar_arrive(&acc_empty[r & 1]);
+            if (release && lane == 0) mbar_arrive(release);
+        };
+        int seen[2] = {0, 0};  // ranges read of each set (bf16), or column range (fp32)
+        bool ok = true;
+        constexpr int kEvery = kBf16 ? kRgHalfRound : kRgRound;
+        for (int j = kEvery; j < steps && ok; j += kEvery) {
+            const int b = kBf16 ? (j / kEvery) & 1 : (j / kEvery - 1) & 1;  // set whose range ends with step j - 1, or range
+            if (kBf16 && b >= sets) continue;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(&acc_full[b], seen[b] & 1, deadline, &status));
+            if (!ok) break;
+            tc_fence_after();
+            if constexpr (kBf16) drain(b, 256 * b, -1, seen[b] == 0, &acc_empty[b]);
+            else drain_direct(kRgMaxE * b, -1, j == kEvery, &acc_empty[b]);
+            ++seen[b];
+        }
+        if (ok && __all_sync(0xFFFFFFFFu, mbar_wait(&done, 0, deadline, &status))) {
+            tc_fence_after();
+            if constexpr (kBf16) {
+                for (int h = 0; h < sets; ++h) drain(h, 256 * h, 256 * h + kRgMaxE, seen[h] == 0, nullptr);
+            } else {
+                drain_direct(kRgMaxE * ((steps - 1) / kRgRound & 1), kRgO12, steps <= kRgRound, nullptr);
+            }
         }
     }
     __syncthreads();
     if (threadIdx.x == 0) a.cta_status[(blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x] = status;
-    if (warp == kRgWarpMma) {
+    if (warp == S::kWarpMma) {
         if (lane == 0) mbar_wait(&done, 0, global_ns() + kRgDrainNs, &status);
         __syncwarp();
         tc_fence_after();
