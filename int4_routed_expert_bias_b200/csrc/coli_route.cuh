@@ -127,9 +127,10 @@ __global__ void __launch_bounds__(kRouteThreads) route_rows_kernel(const __grid_
 // Roles: eight producer warps split W (eight more fp32 x) into swizzled shared
 // memory, the next step's global loads in registers; TMA brings bf16 x; one thread
 // issues MMAs, one TMA; four warps are the epilogue.  Bound by shared
-// memory and the loads of W from L2, which all CTAs of an expert tile read: with
-// 128 bf16 tokens per CTA the scores of 4096 tokens took 63 us, with 256 (a W part
-// split once for twice the tokens) see the figure at the launch.
+// memory: a step of 256 tokens x 128 experts moves about 300 KB through it, 2300
+// cycles, against 1536 of tensor time.  Scores of 4096 bf16 tokens x 256 experts at
+// hidden 6144: 42.5 us (128 tokens per CTA: 63 us; one product of 24-bit scores
+// takes at least 24 us of tensor time).
 constexpr int kRgM = 128, kRgK = 64;
 constexpr int kRgHalf = 256;                   // producer threads of W, and of fp32 x
 constexpr int kRgMaxE = 128;                   // experts per CTA
@@ -390,7 +391,7 @@ route_gemm_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant_
             }
             __syncwarp();
         };
-        // fp32: straight from the accumulator, lane by lane
+        // fp32, and short bf16 calls: straight from the accumulator, lane by lane
         auto drain_direct = [&](uint32_t o0, int o12, bool first, uint64_t* release) {
             const int t = m0 + qd * 32 + lane;
             float* out = a.part + ((size_t)blockIdx.z * a.T + t) * a.Ep + e0;
@@ -398,11 +399,16 @@ route_gemm_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant_
                 float v[16];
                 tmem_ld16(tmem + lanes + o0 + c, v);
                 if (o12 >= 0) {
-                    float v1[16], v2[16];
+                    float v1[16];
                     tmem_ld16(tmem + lanes + o12 + c, v1);
-                    tmem_ld16(tmem + lanes + o12 + ET + c, v2);
+                    if constexpr (!kBf16) {
+                        float v2[16];
+                        tmem_ld16(tmem + lanes + o12 + ET + c, v2);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] += v1[i] + v2[i];
+                        for (int i = 0; i < 16; ++i) v1[i] += v2[i];
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] += v1[i];
                 }
                 if (t < a.T) {
 #pragma unroll
@@ -433,7 +439,9 @@ route_gemm_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant_
         if (ok && __all_sync(0xFFFFFFFFu, mbar_wait(&done, 0, deadline, &status))) {
             tc_fence_after();
             if constexpr (kBf16) {
-                for (int h = 0; h < sets; ++h) drain(h, 256 * h, 256 * h + kRgMaxE, seen[h] == 0, nullptr);
+                // a CTA of few steps has nothing to overlap the detour with (64 tokens x 64 experts: 8.4 us, by rows 9.6)
+                if (sets == 1 && steps <= kRgHalfRound) drain_direct(0, kRgMaxE, true, nullptr);
+                else for (int h = 0; h < sets; ++h) drain(h, 256 * h, 256 * h + kRgMaxE, seen[h] == 0, nullptr);
             } else {
                 drain_direct(kRgMaxE * ((steps - 1) / kRgRound & 1), kRgO12, steps <= kRgRound, nullptr);
             }
@@ -1073,7 +1081,8 @@ __global__ void __launch_bounds__(kRouteThreads, 2) route_select_kernel(const __
         auto score_of = [&](float v) { return a.softmax ? expf(v - zm) / den : 1.0f / (1.0f + expf(-v)); };
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            const float s = a.softmax ? c[i] / den : 1.0f / (1.0f + expf(-c[i]));
+            // (the quotients within 2 units in the last place, as choice_err allows; weights are divided exactly)
+            const float s = a.softmax ? __fdividef(c[i], den) : __fdividef(1.0f, 1.0f + expf(-c[i]));
             const float v = s + bias[i];
             c[i] = v == v ? v : -INFINITY;  // NaN ranks last: the order stays total
         }
