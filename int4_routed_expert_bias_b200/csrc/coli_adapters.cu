@@ -54,15 +54,18 @@ LoPlan lo_plan(const coli_adapters* d, int T, coli_dtype ot)
         const int want = std::max(1, std::min(units, 4 * kSms / p.max_tiles));
         p.cols = (units + want - 1) / want * 32 * kLoWarps;
     } else {
-        // tiles of T tokens over g groups: at most T / 128 whole ones and one more per group
-        p.max_tiles = T / kLtTile + std::min(T, d->n_adapters + 1);
+        // tiles of T tokens over g groups: at most T / 128 whole ones and one more per group; in most batches a
+        // group's last tile is half full, which is what the grid is sized for
+        const int groups = std::min(T, d->n_adapters + 1), likely = std::max(1, T / kLtTile + groups / 2);
+        p.max_tiles = T / kLtTile + groups;
         // about two blocks per SM (4096 tokens: 23 us, one block 27 us); fp32 outputs cut K at 512, which keeps
         // what the tensor core drops per accumulation (2^-24.9 of a sum) below 2^-19.9
-        p.pieces = std::max(1, std::min(K / 256, 2 * kSms / p.max_tiles));
+        p.pieces = std::max(1, std::min(K / 256, 2 * kSms / likely));
         if (ot == COLI_F32) p.pieces = std::max(p.pieces, (K + 511) / 512);
         p.chunk = up((K + p.pieces - 1) / p.pieces, 64);
+        // columns: one block per SM
         const int step = 128, units = (N + step - 1) / step;
-        const int want = std::max(1, std::min(units, kSms / p.max_tiles));
+        const int want = std::max(1, std::min(units, kSms / likely));
         p.cols = (units + want - 1) / want * step;
     }
     p.pieces = (K + p.chunk - 1) / p.chunk;

@@ -291,8 +291,8 @@ struct LtExpand {
 };
 
 // out = base + (scale h) B^T for a tile and `cols` columns.  Grid (tiles, column blocks).
-// Warps 0-7 build the parts of h; then two warps share 32 rows: a thread adds its
-// half of a row of the accumulator to base in the buffer, and the two write the
+// All but the MMA warp build the parts of h; then two of warps 0-7 share 32 rows: a
+// thread adds its half of a row of the accumulator to base in the buffer, and the two write the
 // rows out.  Warps 8-11 bring base, 12-13 B.
 // kCols: columns of a step, 256 bytes of every row (32 columns for fp32 outputs of
 // the highest ranks, whose three parts of h take most of the shared memory).
@@ -386,26 +386,26 @@ __global__ void __launch_bounds__(kLtExpThreads, 1) lt_expand_kernel(const __gri
     const float scale = rank > 0 ? a.scale[ad] : 0.f;
     griddep_wait();
     if (warp == kLtWarpMma) tmem_alloc(&tmem_base, kTmem);
-    if (rank > 0 && warp < 8) {
-        const int chunks = nb * 8;  // 8 rank values each
+    if (rank > 0 && warp < kLtWarpMma) {
+        const int chunks = (rank + 15) / 16 * 2;  // 8 rank values each, what the MMAs read
         const size_t plane = (size_t)a.T * a.R;
-        for (int e = threadIdx.x; e < kLtTile * chunks; e += 256) {
+        for (int e = threadIdx.x; e < kLtTile * chunks; e += kLtWarpMma * 32) {
             const int t = e / chunks, c = e - t * chunks, r = 8 * c;
             float v[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = 0.f;
             if (t < s.count && r < rank) {
                 const float* hp = a.h + (size_t)s.token[t] * a.R + r;
-                for (int p0 = 0; p0 < a.pieces; p0 += 4) {  // eight independent loads at a time
-                    float4 o[4][2];
+                for (int p0 = 0; p0 < a.pieces; p0 += 8) {  // sixteen independent loads at a time
+                    float4 o[8][2];
 #pragma unroll
-                    for (int p = 0; p < 4; ++p)
+                    for (int p = 0; p < 8; ++p)
                         if (p0 + p < a.pieces) {
                             o[p][0] = *reinterpret_cast<const float4*>(hp + (p0 + p) * plane);
                             o[p][1] = *reinterpret_cast<const float4*>(hp + (p0 + p) * plane + 4);
                         }
 #pragma unroll
-                    for (int p = 0; p < 4; ++p)
+                    for (int p = 0; p < 8; ++p)
                         if (p0 + p < a.pieces) {
                             v[0] += o[p][0].x, v[1] += o[p][0].y, v[2] += o[p][0].z, v[3] += o[p][0].w;
                             v[4] += o[p][1].x, v[5] += o[p][1].y, v[6] += o[p][1].z, v[7] += o[p][1].w;
