@@ -115,8 +115,9 @@ template <bool kBf16>
 cudaError_t launch_select(const RouteArgs& a, cudaStream_t s)
 {
     const size_t per = route_token_smem(a.E);
-    // tokens per block, a power of two: one while there are SMs for it, else as many as 48 KB hold
-    const int most = std::max(1, std::min(kRouteWarps, (int)(49152 / per)));
+    // tokens per block, a power of two: one while there are SMs for it, else as many as
+    // 44 KB hold (of the 48 that need no attribute, the kernel's static arrays take 2)
+    const int most = std::max(1, std::min(kRouteWarps, (int)(45056 / per)));
     int tokens = 1;
     while (2 * tokens <= most && tokens * 2 * kRouteSms < a.T) tokens *= 2;
     const dim3 grid((a.T + tokens - 1) / tokens);

@@ -27,7 +27,6 @@ constexpr int kRouteThreads = 256;
 constexpr int kRouteWarps = kRouteThreads / 32;
 constexpr int kRouteMaxGroups = 32;
 constexpr int kRouteSms = 148;      // grid sizing (B200); the results do not depend on it
-constexpr int kRouteRowsMT = 8;     // tokens per pass of the row kernel
 constexpr int kRouteMaxSplits = 64;
 
 struct RouteArgs {

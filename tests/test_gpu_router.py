@@ -107,6 +107,27 @@ def test_shapes(env, T, H, E, k, G, keep, top, bias, renorm, score):
           routed_scale=0.75)
 
 
+@pytest.mark.parametrize("E", [31, 100, 127, 200, 284, 290, 513, 700, 1000])
+def test_long_batches_of_any_expert_count(env, E):
+    """The selection kernel packs as many tokens into a block as its shared memory holds."""
+    x, W, b = inputs(env[1], 2400, 64, E, True, E)
+    check(env, x, W, b, 5)
+
+
+@pytest.mark.parametrize("bf16,H", [(True, 16384), (False, 9000)])
+def test_largest_batch(env, bf16, H):
+    """65536 tokens (the inputs pass 2^31 bytes): rows from all over against the definition."""
+    coli, torch = env
+    T, E, k = 65536, 24, 4
+    x, W, b = inputs(torch, T, H, E, bf16, 3)
+    idx, w = route(env, x, W, b, k, n_group=4, topk_group=2)
+    rows = torch.tensor([0, 1, 255, 256, 32767, 32768, 40000, 65279, 65534, 65535], device="cuda")
+    ridx, rw, _ = reference(x[rows].double().cpu().numpy(), W.double().cpu().numpy(), b.double().cpu().numpy(), k, "sigmoid",
+                            4, 2, 2, True, 1.0)
+    assert np.array_equal(idx[rows].cpu().numpy(), ridx)
+    assert np.abs(w[rows].double().cpu().numpy() - rw).max() < 1e-5
+
+
 @pytest.mark.parametrize("T", [1, 4, 40, 200])
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
 @pytest.mark.parametrize("bias", [False, True])
@@ -191,3 +212,42 @@ def test_streams_graphs_and_repeats(env):
             graph.replay()
             torch.cuda.synchronize()
             assert torch.equal(idx, ref[0]) and torch.equal(w, ref[1])
+
+
+def test_calls_at_once_and_a_graph_with_copies_and_branches(env):
+    """Two streams with a workspace each, many times over, and a captured graph that
+    copies its inputs in and runs two calls on branches."""
+    coli, torch = env
+    cases = []
+    for T, bf16 in ((300, True), (700, False), (3, True)):
+        x, W, b = inputs(torch, T, 1024, 96, bf16, 31 + T)
+        want = route(env, x, W, b, 6, n_group=8, topk_group=3)
+        r = coli.Router(1024, 96, 6, W, b, n_group=8, topk_group=3)
+        ws = torch.empty(coli.router_workspace_size(r, T), dtype=torch.uint8, device="cuda")
+        cases.append((r, x, torch.empty_like(want[0]), torch.empty_like(want[1]), ws, want))
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for st, (r, x, idx, w, ws, _) in zip(streams, cases):
+            coli.router_forward(r, x, idx, w, ws, stream=st)
+    torch.cuda.synchronize()
+    for r, x, idx, w, ws, want in cases:
+        assert torch.equal(idx, want[0]) and torch.equal(w, want[1])
+        idx.zero_(), w.zero_()
+    xin = [torch.zeros_like(c[1]) for c in cases]
+    g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        for buf, c in zip(xin, cases):
+            buf.copy_(c[1])
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            coli.router_forward(cases[0][0], xin[0], cases[0][2], cases[0][3], cases[0][4])
+        for i in (1, 2):
+            coli.router_forward(cases[i][0], xin[i], cases[i][2], cases[i][3], cases[i][4])
+        main.wait_stream(side)
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    for r, x, idx, w, ws, want in cases:
+        assert torch.equal(idx, want[0]) and torch.equal(w, want[1])
