@@ -103,6 +103,43 @@ def test_shapes(env, T, K, N, R, n, xt, ot):
     check(env, T, K, N, R, n, xt, ot)
 
 
+@pytest.mark.parametrize("R", [56, 136, 184, 192, 200, 248])
+@pytest.mark.parametrize("ot", ["bf16", "f32"])
+def test_high_ranks(env, R, ot):
+    """What of the shared memory is left for base rows and B changes with the rank."""
+    check(env, 150, 264, 456, R, 2, ot, ot, ragged=R % 3 == 0)
+    check(env, 30, 264, 456, R, 2, ot, ot, ragged=R % 3 == 0)
+
+
+def test_long_batch_grouping(env):
+    """More tokens than the grouping keeps in registers."""
+    check(env, 9001, 64, 72, 8, 5)
+    check(env, 65536, 8, 8, 8, 1000, "f32", "f32")
+
+
+@pytest.mark.parametrize("xt", ["bf16", "f32"])
+def test_inputs_beyond_32_bit_offsets(env, xt):
+    """x of 2.4e9 values: rows from all over against the formula."""
+    coli, torch = env
+    T, K, N, R, n = 36800, 65536, 16, 8, 3
+    dt = torch.bfloat16 if xt == "bf16" else torch.float32
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    x = torch.empty(T, K, dtype=dt, device="cuda")
+    for i in range(0, T, 4600):
+        x[i:i + 4600] = torch.randn(min(4600, T - i), K, generator=g, device="cuda").to(dt)
+    a = (torch.randn(n, R, K, generator=g, device="cuda") * K ** -0.5).bfloat16()
+    b = torch.randn(n, N, R, generator=g, device="cuda").bfloat16()
+    which = torch.randint(0, n, (T,), generator=g, device="cuda", dtype=torch.int32)
+    ad = coli.Adapters(a, b, torch.ones(n, device="cuda"))
+    ws = torch.empty(coli.adapters_workspace_size(ad, T), dtype=torch.uint8, device="cuda")
+    out = torch.empty(T, N, device="cuda")
+    coli.adapters_forward(ad, x, which, out, ws)
+    rows = torch.tensor([0, 127, 128, 16383, 16384, 32767, 32768, 32769, 36799], device="cuda")
+    want, err = reference(x[rows], a, b, torch.ones(n, device="cuda"), None, which[rows], torch.zeros(len(rows), N, device="cuda"))
+    assert (np.abs(f64(out[rows]) - want) <= err * 1.0001).all()
+
+
 @pytest.mark.parametrize("T", [3, 50, 64, 65, 300])
 def test_in_place_and_full_rank(env, T):
     check(env, T, 512, 384, 32, 4, in_place=True)
@@ -170,3 +207,42 @@ def test_streams_and_graphs(env):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+def test_calls_at_once_and_a_graph_with_copies_and_branches(env):
+    """Streams with a workspace each, many times over, and a captured graph that
+    copies its inputs in and runs calls on branches."""
+    coli, torch = env
+    cases = []
+    for T, dt in ((20, "bf16"), (500, "f32"), (900, "bf16")):
+        t = make(env, T, 512, 384, 32, 4, dt, dt)
+        want = run(env, *t)
+        ad = coli.Adapters(t[1], t[2], t[3], rank=t[4])
+        ws = torch.empty(coli.adapters_workspace_size(ad, T), dtype=torch.uint8, device="cuda")
+        cases.append((ad, t[0], t[5], t[6], torch.empty_like(t[6]), ws, want))
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for st, (ad, x, which, base, out, ws, _) in zip(streams, cases):
+            coli.adapters_forward(ad, x, which, out, ws, base=base, stream=st)
+    torch.cuda.synchronize()
+    for c in cases:
+        assert torch.equal(c[4], c[6])
+        c[4].zero_()
+    xin = [torch.zeros_like(c[1]) for c in cases]
+    g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        for buf, c in zip(xin, cases):
+            buf.copy_(c[1])
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            coli.adapters_forward(cases[0][0], xin[0], cases[0][2], cases[0][4], cases[0][5], base=cases[0][3])
+            coli.adapters_forward(cases[1][0], xin[1], cases[1][2], cases[1][4], cases[1][5], base=cases[1][3])
+        coli.adapters_forward(cases[2][0], xin[2], cases[2][2], cases[2][4], cases[2][5], base=cases[2][3])
+        main.wait_stream(side)
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    for c in cases:
+        assert torch.equal(c[4], c[6])

@@ -121,6 +121,26 @@ def test_without_a_block(env, H):
     check(env, 5, H, "bf16", "f32", post=False, block=False, with_residual=False)
 
 
+def test_largest_batch(env):
+    """65536 x 16384 (2^30 values, 2 GB a tensor): rows from all over."""
+    coli, torch = env
+    T, H = 65536, 16384
+    g = torch.Generator(device="cuda")
+    g.manual_seed(0)
+    d, r = (torch.empty(T, H, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for i in range(0, T, 8192):
+        d[i:i + 8192] = torch.randn(8192, H, generator=g, device="cuda")
+        r[i:i + 8192] = torch.randn(8192, H, generator=g, device="cuda") * 2
+    w = torch.randn(H, generator=g, device="cuda")
+    rows = torch.tensor([0, 1, 32767, 32768, 40001, 65535], device="cuda")
+    new = f64(r[rows]) + f64(d[rows])
+    y = new / np.sqrt((new ** 2).mean(axis=1, keepdims=True) + 1e-5) * f64(w)
+    coli.residual_norm(coli.BlockNorm(H, pre_w=w), r, d, r, d)  # in place
+    torch.cuda.synchronize()
+    assert (np.abs(f64(r[rows]) - new) <= 2.0 ** -8 * np.abs(new) + 1e-5).all()
+    assert (np.abs(f64(d[rows]) - y) <= 2.0 ** -8 * np.abs(y) + 1e-4).all()
+
+
 @pytest.mark.parametrize("scale", [1e-18, 1e-6, 1e6, 1e17])
 def test_magnitudes(env, scale):
     check(env, 4, 1024, "f32", "f32", scale=scale, eps=0.0)
