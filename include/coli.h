@@ -336,8 +336,8 @@ COLI_API size_t coli_router_workspace_size(const coli_router* router, int T);
  * Scores are summed in fp32 (weights to about 1e-6); the selection is that of
  * double-precision sums: a decision closer than fp32 sums can carry is taken
  * from double sums of the experts concerned, so a token routes alike whether it
- * comes alone or in a batch (unless its scores cancel to far below the token's
- * largest score).  A score that is NaN ranks last.  A token with a non-finite
+ * comes alone or in a batch (unless all of its scores cancel to far below the
+ * terms that they sum).  A score that is NaN ranks last.  A token with a non-finite
  * activation gets k distinct experts and unspecified weights; other tokens are
  * not affected.
  * Outputs: topk_idx int32 [T, k], topk_w fp32 [T, k] (device); x 16-byte
