@@ -825,13 +825,14 @@ __device__ __forceinline__ void block_dots(const RouteArgs& a, bool bf16, int t,
 
 // The selection of one token with a few open decisions.  The block calls it; the
 // warp with `owner` decides, all of them sum.  The border groups' leading experts
-// are summed in double and the border drawn again; then the ranking in fp32 is
-// carried on past k until a clear gap, and every run of neighbours without a clear
-// gap is ordered by double sums.  Lane j < k of the owner returns slot j; false:
-// too many open decisions, or the softmax denominator's own error matters
-// (route_exact takes those).
+// are summed in double and the border drawn again; then the ranking in fp32 (slot j
+// < k is my_e, my_c of lane j; taken again where the border moved) is carried on past
+// k until a clear gap, and every run of neighbours without a clear gap is ordered by
+// double sums.  Lane j < k of the owner returns slot j; false: too many open
+// decisions, or the softmax denominator's own error matters (route_exact takes
+// those).  Blocks with such a token are the last to end, so its latency counts.
 __device__ __noinline__ bool route_close(const RouteArgs& a, bool bf16, int t, const float* z_s, const float* c_s, float dz,
-                                         float zm, float den, GroupState gs, bool owner, RouteDots& d, int& my_e, double& my_p)
+                                         float zm, float den, GroupState gs, bool owner, RouteDots& d, float my_c, int& my_e, double& my_p)
 {
     const int lane = threadIdx.x & 31;
     const unsigned full = 0xFFFFFFFFu;
@@ -845,6 +846,7 @@ __device__ __noinline__ bool route_close(const RouteArgs& a, bool bf16, int t, c
     const bool border_open = G > 1 && gs.lo - gs.hi <= 2.f * gs.err;
     bool open = false;
     uint32_t border = 0;
+    const uint32_t kept = gs.kept;
     if (owner) {
         int n = 0;
         if (border_open) {
@@ -901,15 +903,21 @@ __device__ __noinline__ bool route_close(const RouteArgs& a, bool bf16, int t, c
     }
 
     // fp32 ranking until a clear gap behind slot k
-    float my_c = 0.f, my_u = 0.f;
+    float my_u = 0.f;
     int n = 0;
     uint32_t runs = 0;     // lane j and j + 1 without a clear gap
     uint32_t involved = 0;
     if (owner) {
-        my_e = 0;
+        auto score = [&](int e) { return a.softmax ? expf(z_s[e] - zm) / den : 1.0f / (1.0f + expf(-z_s[e])); };
         float prev_c = INFINITY;
         int prev_e = -1;
         const int all = G > 1 ? a.keep * m : E, most = ok ? min(32, all) : 0;
+        if (ok && gs.kept == kept) {
+            n = a.k;
+            const float s = score(my_e);
+            my_u = choice_err(a.softmax, s, my_c, dz), my_p = (double)s;
+            prev_c = __shfl_sync(full, my_c, n - 1), prev_e = __shfl_sync(full, my_e, n - 1);
+        }
         for (; n < most; ++n) {
             float bc = -INFINITY;
             int be = 1 << 20;
@@ -923,7 +931,7 @@ __device__ __noinline__ bool route_close(const RouteArgs& a, bool bf16, int t, c
             const uint32_t top = __reduce_max_sync(full, key);
             const int e = (int)__reduce_min_sync(full, key == top ? (uint32_t)be : 0xFFFFFFFFu);
             const float c = order_value(top);
-            const float s = a.softmax ? expf(z_s[e] - zm) / den : 1.0f / (1.0f + expf(-z_s[e]));
+            const float s = score(e);
             const float u = choice_err(a.softmax, s, c, dz);
             if (lane == n) my_e = e, my_c = c, my_u = u, my_p = (double)s;
             const float last_u = __shfl_sync(full, my_u, n > 0 ? n - 1 : 0);
@@ -943,25 +951,26 @@ __device__ __noinline__ bool route_close(const RouteArgs& a, bool bf16, int t, c
     if ((involved >> lane) & 1u)
         v = choice_exact(a, my_e, d.z(__popc(involved & ((1u << lane) - 1u))), zm, den, my_p);
     __syncwarp();
-    // slot of each: runs stay in place, inside a run by the double sums (equal: lower expert first)
-    const int run = __popc(~runs & ((1u << lane) - 1u));
-    int slot = 0;
+    // runs stay in place, inside a run by the double sums (equal: lower expert first)
+    const uint32_t breaks = ~runs & ((1u << lane) - 1u);  // behind each of them a run begins
+    const int start = breaks ? 32 - __clz(breaks) : 0;
+    const bool mine = (involved >> lane) & 1u;
+    int slot = mine ? start : lane;
     bool close = false;
-    for (int i = 0; i < n; ++i) {
+    for (uint32_t left = involved; left; left &= left - 1) {
+        const int i = __ffs(left) - 1;
         const double o = __shfl_sync(full, v, i), op = __shfl_sync(full, my_p, i);
-        const int oe = __shfl_sync(full, my_e, i), orun = __shfl_sync(full, run, i);
-        if (orun == run) {
+        const int oe = __shfl_sync(full, my_e, i), ostart = __shfl_sync(full, start, i);
+        if (mine && ostart == start) {
             slot += (o > v || (o == v && oe < my_e)) ? 1 : 0;
-            close |= lane < n && i != lane && fabs(o - v) < dd * fabs(op - my_p);
-        } else {
-            slot += i < lane ? 1 : 0;
+            close |= i != lane && fabs(o - v) < dd * fabs(op - my_p);
         }
     }
     if (__any_sync(full, close)) return false;
     int src = lane;
-    for (int i = 0; i < n; ++i) {
-        const int o = __shfl_sync(full, slot, i);
-        if (o == lane) src = i;
+    for (uint32_t left = involved; left; left &= left - 1) {
+        const int i = __ffs(left) - 1;
+        if (__shfl_sync(full, slot, i) == lane) src = i;
     }
     my_e = __shfl_sync(full, my_e, src);
     my_p = __shfl_sync(full, my_p, src);
@@ -1048,7 +1057,7 @@ __global__ void __launch_bounds__(kRouteThreads, 2) route_select_kernel(const __
     unsigned char* st = base + stride - align_up((size_t)E, 16);
 
     // what close decisions need of the usual path
-    float dz = 0.f, zm = -INFINITY, den = 1.f, my_s = 0.f;
+    float dz = 0.f, zm = -INFINITY, den = 1.f, my_s = 0.f, my_c = 0.f;
     int my_e = 0;
     bool open = false;
     GroupState gs{0.f, 0.f, 0.f, 0.f, 0.f, full};
@@ -1145,7 +1154,7 @@ __global__ void __launch_bounds__(kRouteThreads, 2) route_select_kernel(const __
             key[i] = e < E && (G == 1 || ((kept >> (e * a.gmul >> 20)) & 1u)) ? order_key(c[i]) : 0u;
         }
         // k rounds (and one more, for the gap to the first rejected expert)
-        float my_c = 0.f, next_c = -INFINITY;
+        float next_c = -INFINITY;
         int next_e = -1;
         const int rounds = a.k + (a.k < (G > 1 ? a.keep * m : E) ? 1 : 0);
         for (int j = 0; j < rounds; ++j) {
@@ -1194,7 +1203,7 @@ __global__ void __launch_bounds__(kRouteThreads, 2) route_select_kernel(const __
     for (int o = 0; o < nt; ++o)
         if (open_s[o]) {
             const bool owner = warp == o;
-            const bool done = route_close(a, kBf16, t0 + o, z_s, c_s, dz, zm, den, gs, owner, dots, my_e, p);
+            const bool done = route_close(a, kBf16, t0 + o, z_s, c_s, dz, zm, den, gs, owner, dots, my_c, my_e, p);
             if (owner) settled = done;
             __syncthreads();
         }
