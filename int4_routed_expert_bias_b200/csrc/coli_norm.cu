@@ -64,12 +64,12 @@ coli_status coli::check_residual_norm(const coli_block_norm* n, const void* bloc
     if (!known_dtype(xt)) return fail(COLI_ERR_INVALID_ARG, "unknown activation dtype %d", (int)xt);
     if (!known_dtype(rt)) return fail(COLI_ERR_INVALID_ARG, "unknown residual dtype %d", (int)rt);
     if (T < 0 || T > kMaxTokens) return fail(COLI_ERR_INVALID_ARG, "T=%d outside [0, %d]", T, kMaxTokens);
+    if (T == 0) return COLI_OK;  // (empty tensors have no address)
     if (!block_out && (n->post_w || n->gate != COLI_GATE_NONE))
         return fail(COLI_ERR_INVALID_ARG, "block_out is NULL, but the norm has weights or a gate for it");
     if (!residual_out && !normed_out) return fail(COLI_ERR_INVALID_ARG, "neither residual_out nor normed_out is given");
-    if ((normed_out != nullptr) != (n->pre_w != nullptr) && T > 0)
+    if ((normed_out != nullptr) != (n->pre_w != nullptr))
         return fail(COLI_ERR_INVALID_ARG, "normed_out and norm.pre_w go together");
-    if (T == 0) return COLI_OK;
     if (!residual) return fail(COLI_ERR_INVALID_ARG, "residual is NULL");
     if (n->gate != COLI_GATE_NONE && !gate) return fail(COLI_ERR_INVALID_ARG, "gate is NULL");
     const void* ptrs[] = {block_out, residual, residual_out, normed_out, gate};

@@ -65,6 +65,17 @@ def test_empty_batch(coli):
     assert _call(coli, _norm(coli), T=0) == 0
 
 
+def test_empty_tensors(coli):
+    """Tensors without elements have no address: no pointer is looked at."""
+    import torch
+    w = torch.ones(64)
+    n = coli.BlockNorm(64, post_w=w, pre_w=w, gate="token")
+    e = torch.empty(0, 64)
+    assert e.data_ptr() == 0
+    coli.residual_norm(n, e, e.clone(), e.clone(), e.clone(), gate=torch.empty(0), stream=0)
+    assert _call(coli, _norm(coli, gate=1), d=None, r=None, g=None, ro=None, y=None, T=0) == 0
+
+
 def test_binding_refuses_tensors_it_would_misread(coli):
     import torch
     w = torch.ones(64)
