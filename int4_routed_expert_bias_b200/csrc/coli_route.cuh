@@ -989,6 +989,8 @@ __host__ __device__ __forceinline__ size_t route_token_smem(int E)
 // Selection: a block sums the partial scores of `tokens` tokens, one warp per
 // token selects.  kPer = experts per lane.  Latency-bound: k + 1 rounds of a
 // warp-wide maximum (one redux instruction) over order-preserving integer keys.
+// 4096 tokens of 256 experts: 20 us, of which 6 wait for blocks with a close
+// decision.  Two blocks per SM: with three the registers spill (0.5 us slower).
 template <int kPer, bool kBf16>
 __global__ void __launch_bounds__(kRouteThreads, 2) route_select_kernel(const __grid_constant__ RouteArgs a, int tokens)
 {
