@@ -111,3 +111,27 @@ def test_block_status_words(coli):
     b = _Parts(coli, router=None)
     assert f(ctypes.byref(b.block), 1, 4, ctypes.byref(r), ctypes.byref(l)) == 0 and r.value == none
     assert f(ctypes.byref(b.block), 1, 4, None, ctypes.byref(l)) == 1
+
+
+def test_empty_tensors(coli):
+    """A batch of no tokens: tensors without elements have no address, and nothing needs one."""
+    import torch
+    H, F, E, k = 64, 64, 8, 2
+    w = torch.randn(E, H)
+    x, idx, wt = torch.empty(0, H), torch.empty(0, k, dtype=torch.int32), torch.empty(0, k)
+    which, ws = torch.empty(0, dtype=torch.int32), torch.empty(0, dtype=torch.uint8)
+    out = [torch.empty(0, H) for _ in range(3)]
+
+    def experts(n, m):
+        return torch.zeros(E + 1, n, m // 2, dtype=torch.uint8), torch.zeros(E + 1, n, m // 64)
+
+    router = coli.Router(H, E, k, w)
+    adapters = coli.Adapters(torch.zeros(2, 8, H).bfloat16(), torch.zeros(2, H, 8).bfloat16(), torch.ones(2))
+    layer = coli.Layer(H, F, E, k, 1.0, w, torch.zeros(E), *experts(F, H), *experts(F, H), *experts(H, F))
+    norm = coli.BlockNorm(H, pre_w=torch.ones(H))
+    block = coli.Block(layer, norm, norm, router=router, adapters=adapters)
+    coli.router_forward(router, x, idx, wt, ws, stream=0)
+    coli.adapters_forward(adapters, x, which, out[0], ws, base=out[1], stream=0)
+    coli.moe_forward_routed(layer, x, idx, wt, out[0], ws, stream=0)
+    coli.residual_norm(norm, x, out[0], out[1], out[2], stream=0)
+    coli.moe_block_forward(block, x, out[0], out[1], out[2], ws, which=which, stream=0)
