@@ -115,7 +115,8 @@ __global__ void __launch_bounds__(kLoGroupThreads) lo_group_kernel(const __grid_
         if (lane == 31) wsum[0][warp] = ic, wsum[1][warp] = it;
         __syncthreads();
         int pc = 0, pt = 0, all_c = 0, all_t = 0;
-        for (int w = 0; w < kLoGroupThreads / 32; ++w) {
+        const int warps = min(kLoGroupThreads / 32, (bins - b0 + 31) / 32);  // with bins (all 32: 0.6 us more)
+        for (int w = 0; w < warps; ++w) {
             if (w == warp) pc = all_c, pt = all_t;
             all_c += wsum[0][w], all_t += wsum[1][w];
         }
